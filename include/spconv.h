@@ -403,6 +403,170 @@ typedef enum spconv_array {
 int spconv_packed_copy_array(const spconv_packed *p, int which, void *dst, int64_t dst_bytes,
                              int64_t *needed);
 
+/* ------------------------------------------------------------------------
+ * Sequence operators: what a channels-first sequence block needs beside a 1x1
+ * sparse projection.  A 1x1 layer maps N x C x (H*W) positions to
+ * N x M x (H*W); read as N x C x L with L = H*W positions in order, its
+ * output feeds the short causal convolution and the selective scan below, and
+ * the low-rank adapters add each request's own correction to the shared
+ * pruned weights.  (No counterpart in the papers.)
+ *
+ * Conventions beside the ones above:
+ *  - Activations (x, u, delta, z, B, C and their gradients) are of one type,
+ *    spconv_dtype; weights (w, bias, A, D, delta_bias), their gradients and
+ *    the scan's states are float32.  All arithmetic, sums and states are in
+ *    float32; an output is rounded once, when it is stored.
+ *  - Input activations are N x C x L with the positions contiguous and any
+ *    batch and channel stride (in elements); outputs are contiguous.  A
+ *    pointer is aligned to its element type; 16-byte aligned rows run faster.
+ *  - lengths (device int32 [N], or NULL: all L) gives each sequence's number of
+ *    positions, taken as 0..L where it lies outside.  Positions behind it are
+ *    not read; outputs there are written as zeros, and a final state is the
+ *    state after the last position inside (length 0: the initial state).
+ *  - The *_step calls take one position of each of N requests.  Their states
+ *    are updated in place: request n uses state number slots[n] of num_slots
+ *    (device int32 [N]; NULL: number n, then num_slots must be N).  A request
+ *    whose slot lies outside 0..num_slots-1 gets zeros and touches no state.
+ *    Two requests of one call must not share a slot.
+ *  - Outputs must not overlap inputs, unless a call says so.  N = 0, C = 0 or
+ *    L = 0 is valid: what does not depend on any position is still written (a
+ *    final state is the initial state, a weight's gradient is zero).
+ *  - Results do not depend on the order in which blocks run (no atomics).
+ *  - Calls are asynchronous, allocate nothing and can be captured into a CUDA
+ *    graph.  Where a call needs a workspace, its *_workspace function gives the
+ *    bytes for the same arguments (pointers are not looked at); the workspace
+ *    is 16-byte aligned device memory that the caller keeps until the stream
+ *    has passed the call.
+ *  - Errors: INVALID_ARG (a NULL or misaligned pointer, a negative size or
+ *    stride, sizes that do not fit together, an output that overlaps an input,
+ *    a workspace that is too small), UNSUPPORTED (a size beyond the kernels),
+ *    CUDA (the launch failed); all but CUDA before anything is enqueued.
+ * ------------------------------------------------------------------------ */
+
+typedef enum spconv_dtype { SPCONV_F32 = 0, SPCONV_BF16 = 1, SPCONV_F16 = 2 } spconv_dtype;
+
+/*
+ * The short causal convolution along L, one filter of K taps for each channel:
+ *
+ *   p[n,c,:] = state[n,c,0..K-2] followed by x[n,c,0..L-1]   (zeros without state)
+ *   v[n,c,t] = bias[c] + sum_k weight[c,k] * p[n,c,t+k]
+ *   y[n,c,t] = v * sigmoid(v) with silu, else v
+ *
+ * final_state[n,c,:] = the K-1 entries of p that end with the sequence's last
+ * position: the state of a call that continues the sequence.
+ */
+typedef struct spconv_short_conv_args {
+    int32_t N, C, L, K;            /* K = 1..4 taps                                     */
+    int32_t dtype, silu;           /* spconv_dtype; 0 or 1                              */
+    int32_t num_slots, reserved;   /* step: states in the pool                          */
+    int64_t x_stride_n, x_stride_c;
+    int64_t dy_stride_n, dy_stride_c;
+    const void *x;                 /* N x C x L (step: N x C, x_stride_c must be 1)     */
+    const float *weight;           /* C x K                                             */
+    const float *bias;             /* C, or NULL                                        */
+    const void *state;             /* N x C x (K-1), or NULL; not used by step          */
+    const int32_t *lengths;        /* N, or NULL                                        */
+    const int32_t *slots;          /* step: N, or NULL                                  */
+    void *y;                       /* forward, step: N x C x L (step: N x C)            */
+    void *final_state;             /* forward: N x C x (K-1), or NULL                   */
+    void *pool;                    /* step: num_slots x C x (K-1), updated in place     */
+    const void *dy;                /* backward: gradient of y                           */
+    const void *dfinal_state;      /* backward: gradient of final_state, or NULL        */
+    void *dx;                      /* backward: N x C x L                               */
+    void *dstate;                  /* backward: N x C x (K-1), or NULL                  */
+    float *dweight;                /* backward: C x K                                   */
+    float *dbias;                  /* backward: C, or NULL                              */
+    void *workspace;
+    int64_t workspace_bytes;
+} spconv_short_conv_args;
+
+int spconv_short_conv(const spconv_short_conv_args *args, void *stream);
+/* All gradients of one call of spconv_short_conv with the same arguments. */
+int64_t spconv_short_conv_backward_workspace(const spconv_short_conv_args *args);
+int spconv_short_conv_backward(const spconv_short_conv_args *args, void *stream);
+int spconv_short_conv_step(const spconv_short_conv_args *args, void *stream);
+
+/*
+ * The selective state space scan with S states for each channel; channel c
+ * reads B and C of group c / (channels / groups):
+ *
+ *   dt[n,c,t]  = softplus(delta + delta_bias[c])   (or without softplus)
+ *   h[n,c,s]_t = exp(dt * A[c,s]) * h_(t-1) + dt * u[n,c,t] * B[n,g,s,t]
+ *   o[n,c,t]   = sum_s C[n,g,s,t] * h_t + D[c] * u[n,c,t]
+ *   y[n,c,t]   = o * z * sigmoid(z) with z, else o
+ *
+ * h starts from state (zeros without one); final_state is h behind the
+ * sequence's last position.
+ */
+typedef struct spconv_scan_args {
+    int32_t N, channels, L, S, groups; /* S = 1..64; groups divide the channels          */
+    int32_t dtype, softplus;
+    int32_t num_slots;             /* step: states in the pool                          */
+    int64_t u_stride_n, u_stride_c;
+    int64_t delta_stride_n, delta_stride_c;
+    int64_t z_stride_n, z_stride_c;
+    int64_t dy_stride_n, dy_stride_c;
+    int64_t b_stride_n, b_stride_g, b_stride_s; /* step: b_stride_s must be 1            */
+    int64_t c_stride_n, c_stride_g, c_stride_s;
+    const void *u, *delta, *z;     /* N x channels x L (step: N x channels); z or NULL   */
+    const void *B, *C;             /* N x groups x S x L (step: N x groups x S)          */
+    const float *A;                /* channels x S                                      */
+    const float *D;                /* channels, or NULL                                 */
+    const float *delta_bias;       /* channels, or NULL                                 */
+    const float *state;            /* N x channels x S, or NULL; not used by step       */
+    const int32_t *lengths;        /* N, or NULL                                        */
+    const int32_t *slots;          /* step: N, or NULL                                  */
+    void *y;                       /* forward, step: N x channels x L                   */
+    float *final_state;            /* forward: N x channels x S, or NULL                */
+    float *pool;                   /* step: num_slots x channels x S, updated in place  */
+    const void *dy;                /* backward: gradient of y                           */
+    const float *dfinal_state;     /* backward: gradient of final_state, or NULL        */
+    void *du, *ddelta;             /* backward: N x channels x L                        */
+    void *dz;                      /* backward: as z; NULL if and only if z is           */
+    void *dB, *dC;                 /* backward: N x groups x S x L                      */
+    float *dA;                     /* backward: channels x S                            */
+    float *dD, *ddelta_bias;       /* backward: channels, or NULL                       */
+    float *dstate;                 /* backward: N x channels x S, or NULL               */
+    void *workspace;
+    int64_t workspace_bytes;
+} spconv_scan_args;
+
+int64_t spconv_scan_workspace(const spconv_scan_args *args);
+int spconv_scan(const spconv_scan_args *args, void *stream);
+/* All gradients of one call of spconv_scan with the same arguments; the states
+ * are computed again (nothing is kept by the forward call). */
+int64_t spconv_scan_backward_workspace(const spconv_scan_args *args);
+int spconv_scan_backward(const spconv_scan_args *args, void *stream);
+int spconv_scan_step(const spconv_scan_args *args, void *stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection: request n
+ * with adapter i = index[n] of 0..adapters-1 gets
+ *
+ *   out[n,m,p] = y[n,m,p] + scale[i] * sum_r b[i,m,r] * sum_c a[i,r,c] * x[n,c,p]
+ *
+ * and a request with any other index gets out = y.  y holds the shared
+ * projection of x (for pruned weights: what spconv_forward wrote).  Adapters
+ * of a lower rank than R are padded with zeros.
+ */
+typedef struct spconv_adapter_args {
+    int32_t N, P, C, M, R, adapters; /* P positions; R = 1..64                           */
+    int32_t dtype, reserved;
+    int64_t x_stride_n, x_stride_c;  /* P = 1: x_stride_c any; else positions contiguous */
+    const void *x;                 /* N x C x P                                         */
+    const void *a;                 /* adapters x R x C                                  */
+    const void *b;                 /* adapters x M x R                                  */
+    const int32_t *index;          /* N                                                 */
+    const float *scale;            /* adapters, or NULL (all 1)                         */
+    const void *y;                 /* N x M x P, contiguous                             */
+    void *out;                     /* N x M x P; may be y itself                        */
+    void *workspace;
+    int64_t workspace_bytes;
+} spconv_adapter_args;
+
+int64_t spconv_adapter_workspace(const spconv_adapter_args *args);
+int spconv_adapter_add(const spconv_adapter_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,6 +11,10 @@ there is no CPU fallback -- if the library is missing, every call raises.
     w = pack(rowptr, colidx, value, C=..., H=..., W=..., M=..., R=3, S=3,
              stride=1, pad=1)
     y = forward(x_cuda, w)            # x: (N, C, H, W) float32 on the GPU
+
+Beside it stand the operators of a channels-first sequence block whose
+projections are 1x1 layers of this kind (``sequence.py``): the short causal
+convolution, the selective scan and the low-rank adapters of many requests.
 """
 from __future__ import annotations
 
@@ -22,7 +26,8 @@ from . import _lib
 from ._lib import SpconvError, status_string
 
 __all__ = ["pack", "pack_host", "forward", "forward_host", "PackedWeights", "SpconvError", "status_string",
-           "out_extent", "library_path"]
+           "out_extent", "library_path", "short_conv", "short_conv_backward", "short_conv_step",
+           "scan", "scan_backward", "scan_step", "adapter_add"]
 
 
 def library_path() -> str:
@@ -242,3 +247,7 @@ def forward_host(x_host, packed: PackedWeights, out_host, x_dev, out_dev, stream
         ctypes.c_void_p(out_dev.data_ptr()), _stream_ptr(stream))
     _lib.check(rc, "spconv_forward_host")
     return out_host
+
+
+from .sequence import (adapter_add, scan, scan_backward, scan_step, short_conv,  # noqa: E402
+                       short_conv_backward, short_conv_step)

@@ -31,7 +31,11 @@ EXPORTS = ("spconv_pack", "spconv_pack_ex", "spconv_forward", "spconv_forward_ex
            "spconv_status_string",
            "spconv_pack_host", "spconv_device_status", "spconv_selftest_wait",
            "spconv_packed_info_get", "spconv_launch_info_get", "spconv_packed_copy_array",
-           "spconv_trace_read")
+           "spconv_trace_read", "spconv_short_conv", "spconv_short_conv_backward",
+           "spconv_short_conv_backward_workspace", "spconv_short_conv_step",
+           "spconv_scan", "spconv_scan_workspace", "spconv_scan_backward",
+           "spconv_scan_backward_workspace", "spconv_scan_step",
+           "spconv_adapter_add", "spconv_adapter_workspace")
 
 _lock = threading.Lock()
 _lib = None
@@ -64,6 +68,45 @@ class LaunchInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("kernel", "grid_x", "grid_y", "grid_z", "block_threads", "cluster", "push",
                  "group_fast", "tma", "pdl")] + [("smem_bytes", ctypes.c_int64)]
+
+
+def _fields(*groups):
+    """Fields of an argument structure, from names grouped by their C type."""
+    return [(n, t) for t, names in groups for n in names.split()]
+
+
+_i32, _i64, _ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+
+
+class ShortConvArgs(ctypes.Structure):
+    """spconv_short_conv_args"""
+    _fields_ = _fields(
+        (_i32, "N C L K dtype silu num_slots reserved"),
+        (_i64, "x_stride_n x_stride_c dy_stride_n dy_stride_c"),
+        (_ptr, "x weight bias state lengths slots y final_state pool dy dfinal_state dx dstate "
+               "dweight dbias workspace"),
+        (_i64, "workspace_bytes"))
+
+
+class ScanArgs(ctypes.Structure):
+    """spconv_scan_args"""
+    _fields_ = _fields(
+        (_i32, "N channels L S groups dtype softplus num_slots"),
+        (_i64, "u_stride_n u_stride_c delta_stride_n delta_stride_c z_stride_n z_stride_c "
+               "dy_stride_n dy_stride_c b_stride_n b_stride_g b_stride_s c_stride_n c_stride_g "
+               "c_stride_s"),
+        (_ptr, "u delta z B C A D delta_bias state lengths slots y final_state pool dy "
+               "dfinal_state du ddelta dz dB dC dA dD ddelta_bias dstate workspace"),
+        (_i64, "workspace_bytes"))
+
+
+class AdapterArgs(ctypes.Structure):
+    """spconv_adapter_args"""
+    _fields_ = _fields(
+        (_i32, "N P C M R adapters dtype reserved"),
+        (_i64, "x_stride_n x_stride_c"),
+        (_ptr, "x a b index scale y out workspace"),
+        (_i64, "workspace_bytes"))
 
 
 def lib() -> ctypes.CDLL:
@@ -110,6 +153,16 @@ def lib() -> ctypes.CDLL:
         L.spconv_selftest_wait.restype = i
         L.spconv_trace_read.argtypes = [p, ctypes.c_int64]
         L.spconv_trace_read.restype = i
+        for names, args in ((("short_conv", "short_conv_backward", "short_conv_step"), ShortConvArgs),
+                            (("scan", "scan_backward", "scan_step"), ScanArgs),
+                            (("adapter_add",), AdapterArgs)):
+            for n in names:
+                f = getattr(L, "spconv_" + n)
+                f.argtypes, f.restype = [ctypes.POINTER(args), p], i
+        for n, args in (("short_conv_backward", ShortConvArgs), ("scan", ScanArgs),
+                        ("scan_backward", ScanArgs), ("adapter", AdapterArgs)):
+            f = getattr(L, f"spconv_{n}_workspace")
+            f.argtypes, f.restype = [ctypes.POINTER(args)], ctypes.c_int64
         _lib = L
         return L
 

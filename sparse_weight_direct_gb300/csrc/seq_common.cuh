@@ -1,0 +1,147 @@
+// Internal: what the sequence operators (seq_*.cu) share -- element types,
+// vector loads of a row's positions, the activations, and the checks of their
+// C entries.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+#include <initializer_list>
+#include <type_traits>
+
+#include "spconv.h"
+
+#define SPCONV_API extern "C" __attribute__((visibility("default")))
+
+namespace spconv {
+namespace seq {
+
+constexpr int kSMs = 152;
+constexpr int kVec = 8;  // positions a thread holds of a row
+constexpr int kMaxLength = 0x7fffff00;  // positions of a sequence: tiles stay within 32 bits
+
+// ---------------------------------------------------------------- elements
+
+static __device__ __forceinline__ float to_f32(float v) { return v; }
+static __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+static __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <typename T>
+static __device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// V consecutive elements of a row as raw 16-byte words (V * sizeof(T) is a
+// multiple of 16) or, for short runs, as elements.
+template <typename T, int V = kVec>
+struct alignas(V * sizeof(T) >= 16 ? 16 : V * sizeof(T)) Run {
+    T e[V];
+};
+
+// row[t0, t0 + V) where t < end, zeros behind (positions behind `end` are not
+// read unless the run is whole, so what lies there does not matter).
+// vec: the run's address is aligned to the run.
+template <typename T, int V>
+static __device__ __forceinline__ void load_run(Run<T, V> &r, const T *__restrict__ row, int t0,
+                                                int end, bool vec) {
+    if (vec && t0 + V <= end) {
+        r = *reinterpret_cast<const Run<T, V> *>(row + t0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r.e[i] = t0 + i < end ? row[t0 + i] : from_f32<T>(0.f);
+    }
+}
+
+// row[t0, t0 + V) = r where t < L.
+template <typename T, int V>
+static __device__ __forceinline__ void store_run(const Run<T, V> &r, T *__restrict__ row, int t0,
+                                                 int L, bool vec) {
+    if (vec && t0 + V <= L) {
+        *reinterpret_cast<Run<T, V> *>(row + t0) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (t0 + i < L) row[t0 + i] = r.e[i];
+    }
+}
+
+// ---------------------------------------------------------------- activations
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x, relative error about 2^-22.
+static __device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 1 / (1 + e^-v)
+static __device__ __forceinline__ float sigmoid(float v) {
+    return __fdividef(1.f, 1.f + __expf(-v));
+}
+static __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+// d silu / dv
+static __device__ __forceinline__ float silu_grad(float v) {
+    const float s = sigmoid(v);
+    return s * (1.f + v * (1.f - s));
+}
+// log(1 + e^v) = max(v, 0) + log1p(e^-|v|): no overflow, and log1p keeps the
+// small values that step sizes are.
+static __device__ __forceinline__ float softplus(float v) {
+    return fmaxf(v, 0.f) + log1pf(__expf(-fabsf(v)));
+}
+
+// ---------------------------------------------------------------- checks of the C entries
+
+inline bool aligned(const void *p, size_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+inline size_t dtype_size(int dtype) { return dtype == SPCONV_F32 ? 4 : 2; }
+
+// Bytes from the first to behind the last element of an N x C x L tensor.
+inline int64_t extent(int64_t N, int64_t C, int64_t L, int64_t sn, int64_t sc, int64_t size) {
+    if (N <= 0 || C <= 0 || L <= 0) return 0;
+    return ((N - 1) * sn + (C - 1) * sc + L) * size;
+}
+
+inline bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
+    if (!a || !b || an <= 0 || bn <= 0) return false;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
+}
+
+// A stride that 64-bit byte offsets can hold for any valid index.
+inline bool stride_ok(int64_t s) { return s >= 0 && s <= (int64_t)1 << 40; }
+
+// Rows of runs can be read as vectors: base and strides are multiples of
+// 16 bytes.
+inline bool rows_aligned(const void *p, int64_t sn, int64_t sc, size_t size) {
+    return aligned(p, 16) && (sn * (int64_t)size) % 16 == 0 && (sc * (int64_t)size) % 16 == 0;
+}
+
+// Device side of one dtype: f(T{}) with T the element type.
+template <typename F>
+inline int by_dtype(int dtype, F f) {
+    switch (dtype) {
+        case SPCONV_F32: return f(float{});
+        case SPCONV_BF16: return f(__nv_bfloat16{});
+        case SPCONV_F16: return f(__half{});
+    }
+    return SPCONV_ERR_INVALID_ARG;
+}
+
+inline int launch_status() {
+    return cudaGetLastError() == cudaSuccess ? SPCONV_OK : SPCONV_ERR_CUDA;
+}
+
+}  // namespace seq
+}  // namespace spconv

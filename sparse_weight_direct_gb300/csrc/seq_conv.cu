@@ -1,0 +1,450 @@
+// The short causal convolution along the positions of a channels-first
+// sequence, one filter of K = 1..4 taps per channel: forward, backward and the
+// single-token step.
+//
+//   p = (state | x),  v_t = b + sum_k w_k p_(t+k),  y_t = silu(v_t) or v_t
+//
+// With g_t = dy_t * silu'(v_t) inside the sequence and 0 behind it, the
+// gradients are dp_j = sum_k w_k g_(j-k) (dx and dstate are its two parts, and
+// a final state's gradient adds to its last K-1 entries), dw_k = sum g_t
+// p_(t+k) and db = sum g_t.
+//
+// Bound: a few FMAs per element against one read and one write, so the memory
+// bandwidth bounds it.
+#include "seq_common.cuh"
+
+namespace spconv {
+namespace seq {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct ConvParams {
+    const void *x, *state, *dy, *dfinal;
+    const float *weight, *bias;
+    const int32_t *lengths, *slots;
+    void *y, *final_state, *pool, *dx, *dstate;
+    float *dweight, *dbias, *partial;
+    int64_t x_sn, x_sc, dy_sn, dy_sc;
+    int N, C, L, silu, num_slots;
+    int runs;    // runs of kVec positions in a row
+    int tx;      // threads along a row (power of two)
+    int tiles;   // blocks along a row
+    int splits;  // backward: blocks that share a channel
+    int vec_x, vec_y, vec_dy;
+};
+
+static __device__ __forceinline__ int length_of(const int32_t *lengths, int n, int L) {
+    return lengths ? min(max(lengths[n], 0), L) : L;
+}
+
+// The K-1 entries of p before position t0, oldest first (p_(t0) .. p_(t0+K-2)).
+template <typename T, int K>
+static __device__ __forceinline__ void load_before(float (&h)[K > 1 ? K - 1 : 1], const T *row,
+                                                   const T *state_row, int t0) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+        const int t = t0 - (K - 1) + j;
+        h[j] = t >= 0 ? to_f32(row[t]) : state_row ? to_f32(state_row[t + K - 1]) : 0.f;
+    }
+}
+
+// Forward: a thread computes kVec consecutive outputs of one row.  Its K-1
+// inputs to the left are the end of its neighbour's run, so they come from L1.
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p) {
+    const int64_t block = blockIdx.x;
+    const int64_t row_block = block / p.tiles;
+    const int tile = (int)(block - row_block * p.tiles);
+    const int lane = threadIdx.x & (p.tx - 1);
+    const int64_t rowi = row_block * (kThreads / p.tx) + threadIdx.x / p.tx;
+    if (rowi >= (int64_t)p.N * p.C) return;
+    const int n = (int)(rowi / p.C), c = (int)(rowi - (int64_t)n * p.C);
+    const int len = length_of(p.lengths, n, p.L);
+    const T *row = static_cast<const T *>(p.x) + n * p.x_sn + c * p.x_sc;
+    const T *st = p.state ? static_cast<const T *>(p.state) + rowi * (K - 1) : nullptr;
+    const int run = tile * p.tx + lane;
+    if (run < p.runs) {
+        const int t0 = run * kVec;
+        Run<T> out;
+        if (t0 < len) {
+            float w[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k] = p.weight[(int64_t)c * K + k];
+            const float b = p.bias ? p.bias[c] : 0.f;
+            Run<T> in;
+            load_run(in, row, t0, len, p.vec_x);
+            float h[K > 1 ? K - 1 : 1];
+            load_before<T, K>(h, row, st, t0);
+            float s[kVec + K - 1];
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) s[j] = h[j];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) s[K - 1 + i] = to_f32(in.e[i]);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                float v = b;
+#pragma unroll
+                for (int k = 0; k < K; ++k) v = fmaf(w[k], s[i + k], v);
+                if (p.silu) v = silu(v);
+                out.e[i] = from_f32<T>(t0 + i < len ? v : 0.f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) out.e[i] = from_f32<T>(0.f);
+        }
+        store_run(out, static_cast<T *>(p.y) + rowi * p.L, t0, p.L, p.vec_y);
+    }
+    if (K > 1 && p.final_state && tile == 0 && lane == 0) {
+        T *fin = static_cast<T *>(p.final_state) + rowi * (K - 1);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            const int t = len - (K - 1) + j;
+            fin[j] = t >= 0 ? row[t] : st ? st[t + K - 1] : from_f32<T>(0.f);
+        }
+    }
+}
+
+// Backward: a block takes every splits-th group of kThreads runs of one
+// channel over all sequences; a thread holds the inputs around its run, forms
+// g for its kVec positions and the K-1 behind them (which its right neighbour
+// forms too: K-1 in kVec twice is cheaper than an exchange), writes dx and
+// adds to its sums for dw and db.  The sums are joined in a fixed order.
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParams p) {
+    const int c = blockIdx.x / p.splits, split = blockIdx.x - c * p.splits;
+    float w[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = p.weight[(int64_t)c * K + k];
+    const float b = p.bias ? p.bias[c] : 0.f;
+    float sum[K + 1];
+#pragma unroll
+    for (int k = 0; k <= K; ++k) sum[k] = 0.f;
+    const int64_t items = (int64_t)p.N * p.runs;
+    for (int64_t i = (int64_t)split * kThreads + threadIdx.x; i < items;
+         i += (int64_t)p.splits * kThreads) {
+        const int n = (int)(i / p.runs), run = (int)(i - (int64_t)n * p.runs), t0 = run * kVec;
+        const int len = length_of(p.lengths, n, p.L);
+        const int64_t rowi = (int64_t)n * p.C + c;
+        const T *row = static_cast<const T *>(p.x) + n * p.x_sn + c * p.x_sc;
+        const T *drow = static_cast<const T *>(p.dy) + n * p.dy_sn + c * p.dy_sc;
+        const T *st = p.state ? static_cast<const T *>(p.state) + rowi * (K - 1) : nullptr;
+        const T *df = p.dfinal ? static_cast<const T *>(p.dfinal) + rowi * (K - 1) : nullptr;
+        constexpr int kG = kVec + K - 1;
+        float s[kG + K - 1], g[kG];
+        if (t0 < len) {
+            Run<T> in, gin;
+            load_run(in, row, t0, len, p.vec_x);
+            load_run(gin, drow, t0, len, p.vec_dy);
+            float h[K > 1 ? K - 1 : 1];
+            load_before<T, K>(h, row, st, t0);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) s[j] = h[j];
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                s[K - 1 + j] = to_f32(in.e[j]);
+                g[j] = to_f32(gin.e[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                const int t = t0 + kVec + j;
+                s[K - 1 + kVec + j] = t < len ? to_f32(row[t]) : 0.f;
+                g[kVec + j] = t < len ? to_f32(drow[t]) : 0.f;
+            }
+            if (p.silu) {
+#pragma unroll
+                for (int j = 0; j < kG; ++j) {
+                    float v = b;
+#pragma unroll
+                    for (int k = 0; k < K; ++k) v = fmaf(w[k], s[j + k], v);
+                    g[j] = t0 + j < len ? g[j] * silu_grad(v) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                sum[K] += g[j];
+#pragma unroll
+                for (int k = 0; k < K; ++k) sum[k] = fmaf(g[j], s[j + k], sum[k]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kG; ++j) g[j] = 0.f;
+        }
+        Run<T> out;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            float d = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) d = fmaf(w[k], g[j + K - 1 - k], d);
+            const int t = t0 + j, back = t - (len - (K - 1));
+            if (df && t < len && back >= 0) d += to_f32(df[back]);
+            out.e[j] = from_f32<T>(t < len ? d : 0.f);
+        }
+        store_run(out, static_cast<T *>(p.dx) + rowi * p.L, t0, p.L, p.vec_y);
+        if (K > 1 && p.dstate && run == 0) {
+            T *ds = static_cast<T *>(p.dstate) + rowi * (K - 1);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {  // p_j: position j - (K-1)
+                float d = 0.f;
+#pragma unroll
+                for (int k = 0; k <= j; ++k) d = fmaf(w[k], g[j - k], d);
+                if (df && j >= len) d += to_f32(df[j - len]);
+                ds[j] = from_f32<T>(d);
+            }
+        }
+    }
+    __shared__ float part[kThreads / 32][K + 1];
+#pragma unroll
+    for (int k = 0; k <= K; ++k) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum[k] += __shfl_xor_sync(~0u, sum[k], o);
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][k] = sum[k];
+    }
+    __syncthreads();
+    if (threadIdx.x <= K) {
+        float total = 0.f;
+        for (int i = 0; i < kThreads / 32; ++i) total += part[i][threadIdx.x];
+        const int k = threadIdx.x;
+        if (p.splits > 1)
+            p.partial[((int64_t)split * p.C + c) * (K + 1) + k] = total;
+        else if (k < K)
+            p.dweight[(int64_t)c * K + k] = total;
+        else if (p.dbias)
+            p.dbias[c] = total;
+    }
+}
+
+// The blocks' sums of one channel, in their order.
+template <int K>
+__global__ void __launch_bounds__(kThreads) conv_join_kernel(const ConvParams p) {
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= (int64_t)p.C * (K + 1)) return;
+    float total = 0.f;
+    for (int s = 0; s < p.splits; ++s) total += p.partial[(int64_t)s * p.C * (K + 1) + i];
+    const int64_t c = i / (K + 1);
+    const int k = (int)(i - c * (K + 1));
+    if (k < K)
+        p.dweight[c * K + k] = total;
+    else if (p.dbias)
+        p.dbias[c] = total;
+}
+
+// dstate where L = 0: no run exists, the final state is the initial one.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) copy_state_kernel(const void *from, void *to,
+                                                              int64_t count) {
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= count) return;
+    static_cast<T *>(to)[i] = from ? static_cast<const T *>(from)[i] : from_f32<T>(0.f);
+}
+
+// Step: a thread per request and channel.
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvParams p) {
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= (int64_t)p.N * p.C) return;
+    const int n = (int)(i / p.C), c = (int)(i - (int64_t)n * p.C);
+    const int slot = p.slots ? p.slots[n] : n;
+    T *y = static_cast<T *>(p.y) + i;
+    if (slot < 0 || slot >= p.num_slots) {
+        *y = from_f32<T>(0.f);
+        return;
+    }
+    const T x = static_cast<const T *>(p.x)[n * p.x_sn + c];
+    T s[K];
+    T *st = static_cast<T *>(p.pool) + ((int64_t)slot * p.C + c) * (K - 1);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) s[k] = st[k];
+    s[K - 1] = x;
+    float v = p.bias ? p.bias[c] : 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v = fmaf(p.weight[(int64_t)c * K + k], to_f32(s[k]), v);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) st[k] = s[k + 1];
+    *y = from_f32<T>(p.silu ? silu(v) : v);
+}
+
+// ---------------------------------------------------------------- host side
+
+template <typename F>
+int by_taps(int K, F f) {
+    switch (K) {
+        case 1: return f(std::integral_constant<int, 1>{});
+        case 2: return f(std::integral_constant<int, 2>{});
+        case 3: return f(std::integral_constant<int, 3>{});
+        case 4: return f(std::integral_constant<int, 4>{});
+    }
+    return SPCONV_ERR_UNSUPPORTED;
+}
+
+int check_sizes(const spconv_short_conv_args *a) {
+    if (!a || a->N < 0 || a->C < 0 || a->L < 0 || a->K < 1) return SPCONV_ERR_INVALID_ARG;
+    if (a->dtype < SPCONV_F32 || a->dtype > SPCONV_F16 || (a->silu & ~1))
+        return SPCONV_ERR_INVALID_ARG;
+    if (a->K > 4 || a->L > kMaxLength) return SPCONV_ERR_UNSUPPORTED;
+    if (!stride_ok(a->x_stride_n) || !stride_ok(a->x_stride_c) || !stride_ok(a->dy_stride_n) ||
+        !stride_ok(a->dy_stride_c))
+        return SPCONV_ERR_INVALID_ARG;
+    return SPCONV_OK;
+}
+
+ConvParams params_of(const spconv_short_conv_args *a) {
+    const size_t e = dtype_size(a->dtype);
+    ConvParams p{};
+    p.x = a->x; p.state = a->state; p.dy = a->dy; p.dfinal = a->dfinal_state;
+    p.weight = a->weight; p.bias = a->bias;
+    p.lengths = a->lengths; p.slots = a->slots;
+    p.y = a->y; p.final_state = a->final_state; p.pool = a->pool; p.dx = a->dx;
+    p.dstate = a->dstate; p.dweight = a->dweight; p.dbias = a->dbias;
+    p.partial = static_cast<float *>(a->workspace);
+    p.x_sn = a->x_stride_n; p.x_sc = a->x_stride_c;
+    p.dy_sn = a->dy_stride_n; p.dy_sc = a->dy_stride_c;
+    p.N = a->N; p.C = a->C; p.L = a->L; p.silu = a->silu; p.num_slots = a->num_slots;
+    p.runs = (a->L + kVec - 1) / kVec;
+    p.vec_x = rows_aligned(a->x, a->x_stride_n, a->x_stride_c, e);
+    p.vec_dy = rows_aligned(a->dy, a->dy_stride_n, a->dy_stride_c, e);
+    return p;
+}
+
+// Blocks that share a channel's runs in the backward pass: enough to fill the
+// GPU with 8 blocks per SM, none with less than one run per thread.
+int backward_splits(const spconv_short_conv_args *a) {
+    const int64_t items = (int64_t)a->N * ((a->L + kVec - 1) / kVec);
+    const int64_t most = (items + kThreads - 1) / kThreads;
+    const int64_t want = (8 * kSMs + a->C - 1) / a->C;
+    const int64_t s = want < most ? want : most;
+    return s < 1 ? 1 : (int)s;
+}
+
+bool on_elements(const spconv_short_conv_args *a, std::initializer_list<const void *> ps) {
+    for (const void *q : ps)
+        if (q && !aligned(q, dtype_size(a->dtype))) return false;
+    return true;
+}
+
+bool on_words(std::initializer_list<const void *> ps) {
+    for (const void *q : ps)
+        if (q && !aligned(q, 4)) return false;
+    return true;
+}
+
+}  // namespace
+}  // namespace seq
+}  // namespace spconv
+
+using namespace spconv::seq;
+
+SPCONV_API int spconv_short_conv(const spconv_short_conv_args *a, void *stream) {
+    int st = check_sizes(a);
+    if (st) return st;
+    const int64_t rows = (int64_t)a->N * a->C;
+    if (rows == 0) return SPCONV_OK;
+    const size_t e = dtype_size(a->dtype);
+    if (a->L > 0 && (!a->x || !a->weight || !a->y)) return SPCONV_ERR_INVALID_ARG;
+    if (!on_elements(a, {a->x, a->state, a->y, a->final_state}) ||
+        !on_words({a->weight, a->bias, a->lengths}))
+        return SPCONV_ERR_INVALID_ARG;
+    const int64_t xb = extent(a->N, a->C, a->L, a->x_stride_n, a->x_stride_c, e);
+    const int64_t yb = rows * a->L * e, sb = rows * (a->K - 1) * e;
+    if (overlap(a->x, xb, a->y, yb) || overlap(a->x, xb, a->final_state, sb) ||
+        overlap(a->state, sb, a->final_state, sb) || overlap(a->state, sb, a->y, yb) ||
+        overlap(a->y, yb, a->final_state, sb))
+        return SPCONV_ERR_INVALID_ARG;
+    ConvParams p = params_of(a);
+    p.vec_y = rows_aligned(a->y, 0, a->L, e);
+    const int runs = p.runs > 0 ? p.runs : 1;
+    p.tx = 1;
+    while (p.tx < runs && p.tx < kThreads) p.tx *= 2;
+    p.tiles = (runs + p.tx - 1) / p.tx;
+    const int64_t per = kThreads / p.tx, blocks = (rows + per - 1) / per * p.tiles;
+    if (blocks > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
+    return by_dtype(a->dtype, [&](auto t) {
+        return by_taps(a->K, [&](auto k) {
+            conv_kernel<decltype(t), decltype(k)::value>
+                <<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+            return launch_status();
+        });
+    });
+}
+
+SPCONV_API int64_t spconv_short_conv_backward_workspace(const spconv_short_conv_args *a) {
+    if (check_sizes(a) || a->C == 0) return 0;
+    const int s = backward_splits(a);
+    return s > 1 ? (int64_t)s * a->C * (a->K + 1) * 4 : 0;
+}
+
+SPCONV_API int spconv_short_conv_backward(const spconv_short_conv_args *a, void *stream) {
+    int st = check_sizes(a);
+    if (st) return st;
+    if (a->C == 0) return SPCONV_OK;
+    const int64_t rows = (int64_t)a->N * a->C;
+    const size_t e = dtype_size(a->dtype);
+    if (!a->weight || !a->dweight || (rows * a->L > 0 && (!a->x || !a->dy || !a->dx)))
+        return SPCONV_ERR_INVALID_ARG;
+    if (!on_elements(a, {a->x, a->state, a->dy, a->dfinal_state, a->dx, a->dstate}) ||
+        !on_words({a->weight, a->bias, a->lengths, a->dweight, a->dbias}))
+        return SPCONV_ERR_INVALID_ARG;
+    const int64_t need = spconv_short_conv_backward_workspace(a);
+    if (need && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need))
+        return SPCONV_ERR_INVALID_ARG;
+    const int64_t xb = extent(a->N, a->C, a->L, a->x_stride_n, a->x_stride_c, e);
+    const int64_t db = extent(a->N, a->C, a->L, a->dy_stride_n, a->dy_stride_c, e);
+    const int64_t yb = rows * a->L * e, sb = rows * (a->K - 1) * e;
+    if (overlap(a->x, xb, a->dx, yb) || overlap(a->dy, db, a->dx, yb) ||
+        overlap(a->state, sb, a->dx, yb) || overlap(a->dfinal_state, sb, a->dx, yb) ||
+        overlap(a->x, xb, a->dstate, sb) || overlap(a->dy, db, a->dstate, sb) ||
+        overlap(a->state, sb, a->dstate, sb) || overlap(a->dfinal_state, sb, a->dstate, sb) ||
+        overlap(a->dx, yb, a->dstate, sb))
+        return SPCONV_ERR_INVALID_ARG;
+    ConvParams p = params_of(a);
+    p.vec_y = rows_aligned(a->dx, 0, a->L, e);
+    p.splits = backward_splits(a);
+    if ((int64_t)p.splits * a->C > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return by_dtype(a->dtype, [&](auto t) {
+        return by_taps(a->K, [&](auto k) {
+            constexpr int K = decltype(k)::value;
+            using T = decltype(t);
+            const int64_t states = rows * (K - 1);
+            if (a->L == 0 && a->dstate && states > 0)
+                copy_state_kernel<T><<<(unsigned)((states + kThreads - 1) / kThreads), kThreads, 0,
+                                       s>>>(a->dfinal_state, a->dstate, states);
+            conv_backward_kernel<T, K><<<(unsigned)(p.splits * p.C), kThreads, 0, s>>>(p);
+            if (p.splits > 1) {
+                const int64_t count = (int64_t)p.C * (K + 1);
+                conv_join_kernel<K><<<(unsigned)((count + kThreads - 1) / kThreads), kThreads, 0,
+                                      s>>>(p);
+            }
+            return launch_status();
+        });
+    });
+}
+
+SPCONV_API int spconv_short_conv_step(const spconv_short_conv_args *a, void *stream) {
+    int st = check_sizes(a);
+    if (st) return st;
+    if (a->num_slots < 0 || (!a->slots && a->num_slots != a->N) || a->x_stride_c != 1)
+        return SPCONV_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)a->N * a->C;
+    if (rows == 0) return SPCONV_OK;
+    const size_t e = dtype_size(a->dtype);
+    if (!a->x || !a->weight || !a->y || (a->K > 1 && a->num_slots > 0 && !a->pool))
+        return SPCONV_ERR_INVALID_ARG;
+    if (!on_elements(a, {a->x, a->pool, a->y}) || !on_words({a->weight, a->bias, a->slots}))
+        return SPCONV_ERR_INVALID_ARG;
+    const int64_t xb = extent(a->N, a->C, 1, a->x_stride_n, 1, e), yb = rows * e;
+    const int64_t sb = (int64_t)a->num_slots * a->C * (a->K - 1) * e;
+    if (overlap(a->x, xb, a->y, yb) || overlap(a->x, xb, a->pool, sb) ||
+        overlap(a->y, yb, a->pool, sb))
+        return SPCONV_ERR_INVALID_ARG;
+    const ConvParams p = params_of(a);
+    const int64_t blocks = (rows + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
+    return by_dtype(a->dtype, [&](auto t) {
+        return by_taps(a->K, [&](auto k) {
+            conv_step_kernel<decltype(t), decltype(k)::value>
+                <<<(unsigned)blocks, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+            return launch_status();
+        });
+    });
+}
