@@ -153,16 +153,14 @@ def lib() -> ctypes.CDLL:
         L.spconv_selftest_wait.restype = i
         L.spconv_trace_read.argtypes = [p, ctypes.c_int64]
         L.spconv_trace_read.restype = i
-        for names, args in ((("short_conv", "short_conv_backward", "short_conv_step"), ShortConvArgs),
-                            (("scan", "scan_backward", "scan_step"), ScanArgs),
-                            (("adapter_add",), AdapterArgs)):
-            for n in names:
-                f = getattr(L, "spconv_" + n)
-                f.argtypes, f.restype = [ctypes.POINTER(args), p], i
-        for n, args in (("short_conv_backward", ShortConvArgs), ("scan", ScanArgs),
-                        ("scan_backward", ScanArgs), ("adapter", AdapterArgs)):
+        # argument structures: by reference, or packed as bytes
+        for n in ("short_conv", "short_conv_backward", "short_conv_step", "scan", "scan_backward",
+                  "scan_step", "adapter_add"):
+            f = getattr(L, "spconv_" + n)
+            f.argtypes, f.restype = [p, p], i
+        for n in ("short_conv_backward", "scan", "scan_backward", "adapter"):
             f = getattr(L, f"spconv_{n}_workspace")
-            f.argtypes, f.restype = [ctypes.POINTER(args)], ctypes.c_int64
+            f.argtypes, f.restype = [p], ctypes.c_int64
         _lib = L
         return L
 

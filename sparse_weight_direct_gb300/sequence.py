@@ -14,105 +14,105 @@ stream), and a wrong argument raises SpconvError before any work is enqueued.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
 
 from . import _lib
-from ._lib import AdapterArgs, ScanArgs, ShortConvArgs, SpconvError
+from ._lib import SpconvError
 
-_dtypes = {}
+# The argument structures of include/spconv.h without their last two members
+# (workspace, workspace_bytes), packed in one go: filling a ctypes structure
+# field by field costs more than a short kernel runs.
+_pack_conv = struct.Struct("8i4q15P").pack
+_pack_scan = struct.Struct("8i14q25P").pack
+_pack_adapter = struct.Struct("8i2q7P").pack
+_pack_workspace = struct.Struct("Pq").pack
+_no_workspace = _pack_workspace(0, 0)
+
+_torch = None
 
 
-def _torch():
+def _load():
+    """torch and its types, on the first call (the package itself loads without)."""
+    global _torch, _Tensor, _codes, _f32, _i32, _empty, _raw_stream, _current_device, _library
     import torch
-    if not _dtypes:
-        _dtypes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    return torch
+    _Tensor, _empty = torch.Tensor, torch.empty
+    _f32, _i32 = torch.float32, torch.int32
+    _codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _current_device = torch.cuda.current_device
+    _library = _lib.lib()
+    _torch = torch
 
 
 def _fail(what):
     raise SpconvError(_lib.SPCONV_ERR_INVALID_ARG, what)
 
 
-class _Call:
-    """Checks a call's tensors and enqueues it on a stream.  On a stream other
-    than the current one the tensors are marked as used there, so that their
-    memory is not given out again before the stream has passed the call."""
+def _begin(t, name, dims):
+    """The tensor that a call's others go by: its type, its code, its device."""
+    if _torch is None:
+        _load()
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype not in _codes or t.dim() != dims:
+        _fail(f"{name} must be a float32, bfloat16 or float16 CUDA tensor with {dims} dimensions")
+    dtype, device = t.dtype, t.get_device()
+    if device != _current_device():
+        _fail(f"{name} must be on the current CUDA device")
+    return dtype, _codes[dtype], device
 
-    def __init__(self, lead, name, stream):
-        self.torch = torch = _torch()
-        if not (isinstance(lead, torch.Tensor) and lead.is_cuda and lead.dtype in _dtypes):
-            _fail(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
-        self.device, self.dtype = lead.device, lead.dtype
-        self.code = _dtypes[lead.dtype]
-        if self.device.index != torch.cuda.current_device():
-            _fail(f"{name} must be on the current CUDA device")
-        current = torch.cuda.current_stream()
-        if stream is None:
-            self.ptr, self.other = current.cuda_stream, None
-        elif isinstance(stream, int):
-            self.ptr = stream
-            self.other = (torch.cuda.ExternalStream(stream) if stream != current.cuda_stream and stream
-                          else None)
-        else:
-            self.ptr = stream.cuda_stream
-            self.other = stream if self.ptr != current.cuda_stream else None
-        self.used = []
 
-    def _one(self, t, name, shape, dtype):
-        if not (isinstance(t, self.torch.Tensor) and t.dtype == dtype and t.device == self.device
-                and t.shape == shape):
-            _fail(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {self.device}")
-        if self.other is not None:
-            self.used.append(t)
+def _rows(t, name, dtype, device, shape):
+    """Pointer to an activation whose last dimension is contiguous (its other strides are free)."""
+    if not isinstance(t, _Tensor) or t.dtype != dtype or t.get_device() != device or t.shape != shape:
+        _fail(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on CUDA device {device}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        _fail(f"{name} must be contiguous along its last dimension")
+    return t.data_ptr()
 
-    def rows(self, t, name, shape):
-        """An activation whose last dimension is contiguous: its pointer (strides are the caller's)."""
-        self._one(t, name, shape, self.dtype)
-        if shape[-1] > 1 and t.stride(-1) != 1:
-            _fail(f"{name} must be contiguous along its last dimension")
-        return t.data_ptr()
 
-    def whole(self, t, name, shape, dtype=None):
-        """A contiguous tensor or None: its pointer."""
-        if t is None:
-            return None
-        self._one(t, name, shape, dtype or self.dtype)
-        if not t.is_contiguous():
-            _fail(f"{name} must be contiguous")
-        return t.data_ptr()
+def _whole(t, name, dtype, device, shape):
+    """Pointer to a contiguous tensor, 0 for None."""
+    if t is None:
+        return 0
+    if not isinstance(t, _Tensor) or t.dtype != dtype or t.get_device() != device or t.shape != shape:
+        _fail(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on CUDA device {device}")
+    if not t.is_contiguous():
+        _fail(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def new(self, shape, dtype=None):
-        t = self.torch.empty(shape, dtype=dtype or self.dtype, device=self.device)
-        if self.other is not None:
-            self.used.append(t)
-        return t
 
-    def out(self, t, name, shape):
-        if t is None:
-            return self.new(shape)
-        self.whole(t, name, shape)
-        return t
-
-    def workspace(self, args, function):
-        need = getattr(_lib.lib(), function)(ctypes.byref(args))
-        if need:
-            t = self.new((need,), self.torch.uint8)
-            args.workspace, args.workspace_bytes = t.data_ptr(), need
-            return t  # kept until the launches are enqueued
-        return None
-
-    def run(self, function, args):
-        rc = getattr(_lib.lib(), function)(ctypes.byref(args), self.ptr)
-        if rc:
-            _lib.check(rc, function)
-        for t in self.used:
-            t.record_stream(self.other)
+def _new(shape, dtype, device):
+    return _empty(shape, dtype=dtype, device=device)
 
 
 def _dims(t, count, name):
-    if getattr(t, "dim", lambda: -1)() != count:
-        _fail(f"{name} must have {count} dimensions")
+    if not isinstance(t, _Tensor) or t.dim() != count:
+        _fail(f"{name} must be a tensor with {count} dimensions")
     return t.shape
+
+
+def _run(function, args, device, stream, tensors, query=None):
+    """Enqueues a call on its stream.  On a stream other than the current one the
+    call's tensors are marked as used there, so that their memory is not given
+    out again before the stream has passed the call."""
+    current = _raw_stream(device)
+    ptr = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    workspace = None
+    if query is not None and (need := query(args + _no_workspace)):
+        workspace = _empty(need, dtype=_torch.uint8, device=device)
+        args += _pack_workspace(workspace.data_ptr(), need)
+    else:
+        args += _no_workspace
+    rc = function(args, ptr)
+    if rc:
+        _lib.check(rc, function.__name__)
+    if ptr != current:
+        on = stream
+        if isinstance(stream, int):
+            on = _torch.cuda.ExternalStream(ptr) if ptr else _torch.cuda.default_stream(device)
+        for t in (*tensors, workspace):
+            if t is not None:
+                t.record_stream(on)
 
 
 def short_conv(x, weight, bias=None, *, silu: bool = True, state=None, final_state=None,
@@ -123,21 +123,21 @@ def short_conv(x, weight, bias=None, *, silu: bool = True, state=None, final_sta
     float32; state: (N, C, K-1), the inputs before x; lengths: (N,) int32, outputs behind
     them are zero; final_state (optional, same shape as state): overwritten
     with the state behind the last position.  Returns y (``out`` if given)."""
-    N, C, L = _dims(x, 3, "x")
+    dt, code, dev = _begin(x, "x", 3)
+    shape = N, C, L = x.shape
     K = _dims(weight, 2, "weight")[1]
-    c = _Call(x, "x", stream)
-    f32, i32 = c.torch.float32, c.torch.int32
-    a = ShortConvArgs(N, C, L, K, c.code, bool(silu))
-    a.x, a.x_stride_n, a.x_stride_c = c.rows(x, "x", x.shape), x.stride(0), x.stride(1)
-    a.weight = c.whole(weight, "weight", (C, K), f32)
-    a.bias = c.whole(bias, "bias", (C,), f32)
-    a.state = c.whole(state, "state", (N, C, K - 1))
-    a.final_state = c.whole(final_state, "final_state", (N, C, K - 1))
-    a.lengths = c.whole(lengths, "lengths", (N,), i32)
-    y = c.out(out, "out", (N, C, L))
-    a.y = y.data_ptr()
-    c.run("spconv_short_conv", a)
-    return y
+    st = (N, C, K - 1)
+    if out is None:
+        out = _new(shape, dt, dev)
+    args = _pack_conv(
+        N, C, L, K, code, silu, 0, 0, x.stride(0), x.stride(1), 0, 0,
+        _rows(x, "x", dt, dev, shape), _whole(weight, "weight", _f32, dev, (C, K)),
+        _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
+        _whole(lengths, "lengths", _i32, dev, (N,)), 0, _whole(out, "out", dt, dev, shape),
+        _whole(final_state, "final_state", dt, dev, st), 0, 0, 0, 0, 0, 0, 0)
+    _run(_library.spconv_short_conv, args, dev, stream,
+         (x, weight, bias, state, lengths, out, final_state))
+    return out
 
 
 def short_conv_backward(dy, x, weight, bias=None, *, silu: bool = True, state=None,
@@ -145,28 +145,24 @@ def short_conv_backward(dy, x, weight, bias=None, *, silu: bool = True, state=No
     """Gradients of ``short_conv`` called with the same arguments, from those of
     y (dy) and, optionally, of final_state: (dx, dweight, dbias, dstate), with
     None for dbias without a bias and for dstate without a state."""
-    N, C, L = _dims(x, 3, "x")
+    dt, code, dev = _begin(x, "x", 3)
+    shape = N, C, L = x.shape
     K = _dims(weight, 2, "weight")[1]
-    c = _Call(x, "x", stream)
-    f32, i32 = c.torch.float32, c.torch.int32
-    a = ShortConvArgs(N, C, L, K, c.code, bool(silu))
-    a.x, a.x_stride_n, a.x_stride_c = c.rows(x, "x", x.shape), x.stride(0), x.stride(1)
-    a.dy = c.rows(dy, "dy", x.shape)
-    a.dy_stride_n, a.dy_stride_c = dy.stride(0), dy.stride(1)
-    a.weight = c.whole(weight, "weight", (C, K), f32)
-    a.bias = c.whole(bias, "bias", (C,), f32)
-    a.state = c.whole(state, "state", (N, C, K - 1))
-    a.dfinal_state = c.whole(dfinal_state, "dfinal_state", (N, C, K - 1))
-    a.lengths = c.whole(lengths, "lengths", (N,), i32)
-    dx, dw = c.new((N, C, L)), c.new((C, K), f32)
-    db = c.new((C,), f32) if bias is not None else None
-    ds = c.new((N, C, K - 1)) if state is not None else None
-    a.dx, a.dweight = dx.data_ptr(), dw.data_ptr()
-    a.dbias = db.data_ptr() if db is not None else None
-    a.dstate = ds.data_ptr() if ds is not None else None
-    keep = c.workspace(a, "spconv_short_conv_backward_workspace")
-    c.run("spconv_short_conv_backward", a)
-    del keep
+    st = (N, C, K - 1)
+    dy_at = _rows(dy, "dy", dt, dev, shape)
+    dx, dw = _new(shape, dt, dev), _new((C, K), _f32, dev)
+    db = _new((C,), _f32, dev) if bias is not None else None
+    ds = _new(st, dt, dev) if state is not None else None
+    args = _pack_conv(
+        N, C, L, K, code, silu, 0, 0, x.stride(0), x.stride(1), dy.stride(0), dy.stride(1),
+        _rows(x, "x", dt, dev, shape), _whole(weight, "weight", _f32, dev, (C, K)),
+        _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
+        _whole(lengths, "lengths", _i32, dev, (N,)), 0, 0, 0, 0, dy_at,
+        _whole(dfinal_state, "dfinal_state", dt, dev, st), dx.data_ptr(),
+        0 if ds is None else ds.data_ptr(), dw.data_ptr(), 0 if db is None else db.data_ptr())
+    _run(_library.spconv_short_conv_backward, args, dev, stream,
+         (dy, x, weight, bias, state, lengths, dfinal_state, dx, dw, db, ds),
+         _library.spconv_short_conv_backward_workspace)
     return dx, dw, db, ds
 
 
@@ -176,51 +172,48 @@ def short_conv_step(x, state, weight, bias=None, *, silu: bool = True, slots=Non
     (num_slots, C, K-1) moved on in place.  Request n uses state slots[n] ((N,)
     int32; None: number n); one whose slot is outside gets zeros and changes
     nothing."""
-    N, C = _dims(x, 2, "x")
+    dt, code, dev = _begin(x, "x", 2)
+    shape = N, C = x.shape
     K = _dims(weight, 2, "weight")[1]
-    c = _Call(x, "x", stream)
-    f32, i32 = c.torch.float32, c.torch.int32
     pool = _dims(state, 3, "state")[0]
-    a = ShortConvArgs(N, C, 1, K, c.code, bool(silu), pool)
-    a.x, a.x_stride_n, a.x_stride_c = c.rows(x, "x", x.shape), x.stride(0), 1
-    a.pool = c.whole(state, "state", (pool, C, K - 1))
-    a.weight = c.whole(weight, "weight", (C, K), f32)
-    a.bias = c.whole(bias, "bias", (C,), f32)
-    a.slots = c.whole(slots, "slots", (N,), i32)
-    y = c.out(out, "out", (N, C))
-    a.y = y.data_ptr()
-    c.run("spconv_short_conv_step", a)
-    return y
+    if out is None:
+        out = _new(shape, dt, dev)
+    args = _pack_conv(
+        N, C, 1, K, code, silu, pool, 0, x.stride(0), 1, 0, 0, _rows(x, "x", dt, dev, shape),
+        _whole(weight, "weight", _f32, dev, (C, K)), _whole(bias, "bias", _f32, dev, (C,)), 0, 0,
+        _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape), 0,
+        _whole(state, "state", dt, dev, (pool, C, K - 1)), 0, 0, 0, 0, 0, 0)
+    _run(_library.spconv_short_conv_step, args, dev, stream, (x, weight, bias, slots, out, state))
+    return out
 
 
-def _scan_args(c, u, delta, A, B, C, D, z, delta_bias, softplus, step, pool):
-    """The arguments that the scan's calls share; B and C: (N, S[, L]) or
-    (N, groups, S[, L])."""
-    f32 = c.torch.float32
+def _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, step, pool, dy=None):
+    """What the scan's calls have in common, up to the pointer to delta_bias, and S.
+    B and C: (N, S[, L]) or (N, groups, S[, L])."""
     shape = u.shape
     N, ch = shape[0], shape[1]
+    L = 1 if step else shape[2]
     S = _dims(A, 2, "A")[1]
-    tail = (S,) if step else (S, shape[2])
-    G = B.shape[1] if getattr(B, "dim", lambda: -1)() == 2 + len(tail) else 1
-    if G < 1 or ch % G:
-        _fail("the groups of B and C must divide the channels")
-    a = ScanArgs(N, ch, 1 if step else shape[2], S, G, c.code, bool(softplus), pool)
-    for t, name in ((u, "u"), (delta, "delta"), (z, "z")):
-        if t is not None:
-            setattr(a, name, c.rows(t, name, shape))
-            setattr(a, name + "_stride_n", t.stride(0))
-            setattr(a, name + "_stride_c", 1 if step else t.stride(1))
-    for t, name, low in ((B, "B", "b"), (C, "C", "c")):
-        grouped = getattr(t, "dim", lambda: -1)() == 2 + len(tail)
-        p = c.rows(t, name, (N, G) + tail if grouped else (N,) + tail)
-        setattr(a, name, p)
-        setattr(a, low + "_stride_n", t.stride(0))
-        setattr(a, low + "_stride_g", t.stride(1) if grouped else 0)
-        setattr(a, low + "_stride_s", 1 if step else t.stride(-2))
-    a.A = c.whole(A, "A", (ch, S), f32)
-    a.D = c.whole(D, "D", (ch,), f32)
-    a.delta_bias = c.whole(delta_bias, "delta_bias", (ch,), f32)
-    return a, S
+    tail = (S,) if step else (S, L)
+    both, strides, G = [], [], 1
+    for t, name in ((B, "B"), (C, "C")):
+        grouped = isinstance(t, _Tensor) and t.dim() == 2 + len(tail)
+        if grouped and name == "B":
+            G = t.shape[1]
+            if G < 1 or ch % G:
+                _fail("the groups of B and C must divide the channels")
+        both.append(_rows(t, name, dt, dev, (N, G) + tail if grouped else (N,) + tail))
+        strides += (t.stride(0), t.stride(1) if grouped else 0, 1 if step else t.stride(-2))
+    if G > 1 and not grouped:
+        _fail("B and C must have the same groups")
+    own = [_rows(u, "u", dt, dev, shape), _rows(delta, "delta", dt, dev, shape),
+           0 if z is None else _rows(z, "z", dt, dev, shape)]
+    rows = []
+    for t in (u, delta, z, dy):
+        rows += (0, 0) if t is None else (t.stride(0), 1 if step else t.stride(1))
+    return (N, ch, L, S, G, code, softplus, pool, *rows, *strides, *own, *both,
+            _whole(A, "A", _f32, dev, (ch, S)), _whole(D, "D", _f32, dev, (ch,)),
+            _whole(delta_bias, "delta_bias", _f32, dev, (ch,))), S
 
 
 def scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool = True, state=None,
@@ -235,20 +228,20 @@ def scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool =
 
     lengths: (N,) int32, outputs behind them are zero; final_state (optional):
     overwritten with h behind the last position.  Returns y."""
-    shape = _dims(u, 3, "u")
-    c = _Call(u, "u", stream)
-    f32, i32 = c.torch.float32, c.torch.int32
-    a, S = _scan_args(c, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0)
+    dt, code, dev = _begin(u, "u", 3)
+    shape = u.shape
+    given, S = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0)
     states = (shape[0], shape[1], S)
-    a.state = c.whole(state, "state", states, f32)
-    a.final_state = c.whole(final_state, "final_state", states, f32)
-    a.lengths = c.whole(lengths, "lengths", (shape[0],), i32)
-    y = c.out(out, "out", shape)
-    a.y = y.data_ptr()
-    keep = c.workspace(a, "spconv_scan_workspace")
-    c.run("spconv_scan", a)
-    del keep
-    return y
+    if out is None:
+        out = _new(shape, dt, dev)
+    args = _pack_scan(
+        *given, _whole(state, "state", _f32, dev, states),
+        _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, _whole(out, "out", dt, dev, shape),
+        _whole(final_state, "final_state", _f32, dev, states), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    _run(_library.spconv_scan, args, dev, stream,
+         (u, delta, A, B, C, D, z, delta_bias, state, lengths, out, final_state),
+         _library.spconv_scan_workspace)
+    return out
 
 
 def scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool = True,
@@ -256,27 +249,27 @@ def scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, sof
     """Gradients of ``scan`` called with the same arguments, from those of y (dy)
     and, optionally, of final_state: a dict of du, ddelta, dA, dB, dC, dD, dz,
     ddelta_bias and dstate, None for an argument that was not given."""
-    shape = _dims(u, 3, "u")
-    c = _Call(u, "u", stream)
-    f32, i32 = c.torch.float32, c.torch.int32
-    a, S = _scan_args(c, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0)
-    a.dy = c.rows(dy, "dy", shape)
-    a.dy_stride_n, a.dy_stride_c = dy.stride(0), dy.stride(1)
+    dt, code, dev = _begin(u, "u", 3)
+    shape = u.shape
+    dy_at = _rows(dy, "dy", dt, dev, shape)
+    given, S = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0,
+                            dy)
     states = (shape[0], shape[1], S)
-    a.state = c.whole(state, "state", states, f32)
-    a.dfinal_state = c.whole(dfinal_state, "dfinal_state", states, f32)
-    a.lengths = c.whole(lengths, "lengths", (shape[0],), i32)
-    g = dict(du=c.new(shape), ddelta=c.new(shape), dA=c.new(A.shape, f32), dB=c.new(B.shape),
-             dC=c.new(C.shape), dD=c.new(D.shape, f32) if D is not None else None,
-             dz=c.new(shape) if z is not None else None,
-             ddelta_bias=c.new(delta_bias.shape, f32) if delta_bias is not None else None,
-             dstate=c.new(states, f32) if state is not None else None)
-    for name, t in g.items():
-        if t is not None:
-            setattr(a, name, t.data_ptr())
-    keep = c.workspace(a, "spconv_scan_backward_workspace")
-    c.run("spconv_scan_backward", a)
-    del keep
+    g = dict(du=_new(shape, dt, dev), ddelta=_new(shape, dt, dev), dA=_new(A.shape, _f32, dev),
+             dB=_new(B.shape, dt, dev), dC=_new(C.shape, dt, dev),
+             dD=None if D is None else _new(D.shape, _f32, dev),
+             dz=None if z is None else _new(shape, dt, dev),
+             ddelta_bias=None if delta_bias is None else _new(delta_bias.shape, _f32, dev),
+             dstate=None if state is None else _new(states, _f32, dev))
+    at = {k: 0 if t is None else t.data_ptr() for k, t in g.items()}
+    args = _pack_scan(
+        *given, _whole(state, "state", _f32, dev, states),
+        _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, 0, 0, 0, dy_at,
+        _whole(dfinal_state, "dfinal_state", _f32, dev, states), at["du"], at["ddelta"], at["dz"],
+        at["dB"], at["dC"], at["dA"], at["dD"], at["ddelta_bias"], at["dstate"])
+    _run(_library.spconv_scan_backward, args, dev, stream,
+         (dy, u, delta, A, B, C, D, z, delta_bias, state, lengths, dfinal_state, *g.values()),
+         _library.spconv_scan_backward_workspace)
     return g
 
 
@@ -286,17 +279,18 @@ def scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, soft
     (N, S) or (N, groups, S) -> y (N, channels); ``state`` (num_slots,
     channels, S) float32 is moved on in place.  slots as for
     ``short_conv_step``."""
-    N, ch = _dims(u, 2, "u")
-    c = _Call(u, "u", stream)
-    f32, i32 = c.torch.float32, c.torch.int32
+    dt, code, dev = _begin(u, "u", 2)
+    shape = N, ch = u.shape
     pool = _dims(state, 3, "state")[0]
-    a, S = _scan_args(c, u, delta, A, B, C, D, z, delta_bias, softplus, True, pool)
-    a.pool = c.whole(state, "state", (pool, ch, S), f32)
-    a.slots = c.whole(slots, "slots", (N,), i32)
-    y = c.out(out, "out", (N, ch))
-    a.y = y.data_ptr()
-    c.run("spconv_scan_step", a)
-    return y
+    given, S = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, True, pool)
+    if out is None:
+        out = _new(shape, dt, dev)
+    args = _pack_scan(
+        *given, 0, 0, _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape),
+        0, _whole(state, "state", _f32, dev, (pool, ch, S)), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    _run(_library.spconv_scan_step, args, dev, stream,
+         (u, delta, A, B, C, D, z, delta_bias, slots, out, state))
+    return out
 
 
 def adapter_add(y, x, a, b, index, *, scale=None, out=None, stream=None):
@@ -306,27 +300,23 @@ def adapter_add(y, x, a, b, index, *, scale=None, out=None, stream=None):
     projection's output, (N, M, P) or (N, M); a: (adapters, R, C) and b:
     (adapters, M, R) of x's type, R = 1..64; index: (N,) int32; scale:
     (adapters,) float32, 1 if None.  out may be y itself.  Returns out."""
-    c = _Call(x, "x", stream)
-    if x.dim() not in (2, 3):
-        _fail("x must have 2 or 3 dimensions")
+    single = getattr(x, "ndim", 0) == 2
+    dt, code, dev = _begin(x, "x", 2 if single else 3)
     N, C = x.shape[0], x.shape[1]
-    P = x.shape[2] if x.dim() == 3 else 1
+    P = 1 if single else x.shape[2]
     K, R, _ = _dims(a, 3, "a")
     M = _dims(b, 3, "b")[1]
-    f32, i32 = c.torch.float32, c.torch.int32
-    g = AdapterArgs(N, P, C, M, R, K, c.code)
-    g.x, g.x_stride_n, g.x_stride_c = c.rows(x, "x", x.shape), x.stride(0), x.stride(1)
-    g.a = c.whole(a, "a", (K, R, C))
-    g.b = c.whole(b, "b", (K, M, R))
-    g.index = c.whole(index, "index", (N,), i32)
-    g.scale = c.whole(scale, "scale", (K,), f32)
-    shape = (N, M, P) if x.dim() == 3 else (N, M)
-    g.y = c.whole(y, "y", shape)
+    shape = (N, M) if single else (N, M, P)
     if y is None:
         _fail("y must be given")
-    out = c.out(out, "out", shape)
-    g.out = out.data_ptr()
-    keep = c.workspace(g, "spconv_adapter_workspace")
-    c.run("spconv_adapter_add", g)
-    del keep
+    y_at = _whole(y, "y", dt, dev, shape)
+    if out is None:
+        out = _new(shape, dt, dev)
+    args = _pack_adapter(
+        N, P, C, M, R, K, code, 0, x.stride(0), x.stride(1), _rows(x, "x", dt, dev, x.shape),
+        _whole(a, "a", dt, dev, (K, R, C)), _whole(b, "b", dt, dev, (K, M, R)),
+        _whole(index, "index", _i32, dev, (N,)), _whole(scale, "scale", _f32, dev, (K,)), y_at,
+        _whole(out, "out", dt, dev, shape))
+    _run(_library.spconv_adapter_add, args, dev, stream, (y, x, a, b, index, scale, out),
+         _library.spconv_adapter_workspace)
     return out
