@@ -15,62 +15,80 @@ namespace spconv {
 namespace seq {
 namespace {
 
-// One pass over a chunk of positions with the states in registers; the y of a
-// position is the sum of the four lanes' parts, joined through shared memory
-// once per tile.
-template <typename T, int SPT>
+// Shared memory of a block, in floats: B and C of two tiles, each channel's
+// {dt, dt, dt u, dt u} and each lane's part of its positions' outputs.
+constexpr int kTile = 4 * kVec;
+constexpr int kStepPitch = kTile + 5;  // rows of 16 bytes: odd, so that eight channels' reads
+                                       // of one position meet no bank twice
+constexpr int kPartPitch = kTile + 4;
+template <int SPT, bool ENDS>
+constexpr int scan_smem() {
+    return (ENDS ? 2 : 4) * kTile * 4 * SPT + kScanChannels * 4 * kStepPitch +
+           (ENDS ? 0 : kScanThreads * kPartPitch);
+}
+
+// One pass over a chunk of positions with the states in registers.
+// ENDS: from zero states, only what the chunk leaves and the sum of its step
+// sizes.  Otherwise the outputs: the y of a position is the sum of the four
+// lanes' parts, joined through shared memory once per tile.
+template <typename T, int SPT, bool ENDS>
 __global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanParams p) {
-    constexpr int VE = 8, TT = 4 * VE, SP = 4 * SPT;
+    constexpr int VE = kVec, TT = kTile, SP = 4 * SPT, NP = Pairs<SPT>::N;
     extern __shared__ __align__(16) float sm[];
-    float *bc = sm;                                   // [2 buffers][2][TT][SP]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = lane >> 2, j = lane & 3;
-    float *own = sm + 4 * TT * SP + warp * (8 * (TT + 2) * 2 + 32 * (TT + 4));
-    float2 *dtu = reinterpret_cast<float2 *>(own) + ch * (TT + 2);  // {dt, dt * u}
-    float *part = own + 8 * (TT + 2) * 2;             // [8 channels * 4 lanes][TT + 4]
+    constexpr int kBuf = (ENDS ? 1 : 2) * TT * SP;
+    float *bc = sm;                                   // [2 buffers][B, C][TT][SP]
+    const int lane = threadIdx.x & 31, j = lane & 3;
+    ulonglong2 *steps = reinterpret_cast<ulonglong2 *>(sm + 2 * kBuf) +
+                        (threadIdx.x >> 2) * kStepPitch;
+    float *parts = sm + 2 * kBuf + kScanChannels * 4 * kStepPitch;
 
     const int cb = blockIdx.x, chunk = blockIdx.z;
     const ScanPlace at(p, blockIdx.y, cb);
-    const int first = chunk * p.chunk_len, stop = min(p.L, first + p.chunk_len);
+    const int first = chunk * p.chunk_len, stop = first + min(p.L - first, p.chunk_len);
     const int end = max(min(at.len, stop), first), row_end = at.valid ? end : 0;
     const int64_t row = (int64_t)at.n * p.channels + at.c;
     const T *ur = static_cast<const T *>(p.u) + at.n * p.u_sn + at.c * p.u_sc;
     const T *dr = static_cast<const T *>(p.delta) + at.n * p.d_sn + at.c * p.d_sc;
-    const T *zr = p.z ? static_cast<const T *>(p.z) + at.n * p.z_sn + at.c * p.z_sc : nullptr;
+    const T *zr = !ENDS && p.z ? static_cast<const T *>(p.z) + at.n * p.z_sn + at.c * p.z_sc
+                               : nullptr;
     T *yr = static_cast<T *>(p.y) + row * p.L;
     const float bias = p.delta_bias ? p.delta_bias[at.c] : 0.f, D = p.D ? p.D[at.c] : 0.f;
     const int s0 = j * SPT;
 
-    float A[SPT], h[SPT];
-    load_states<SPT>(A, p.A + (int64_t)at.c * p.S, s0, p.S);
-#pragma unroll
-    for (int i = 0; i < SPT; ++i) A[i] *= kLog2e;
-    if (p.chunks > 1)
-        load_states<SPT>(h, p.h_chunk + (((int64_t)at.n * p.chunks + chunk) * p.channels + at.c) * p.S,
-                         s0, p.S);
+    Pairs<SPT> A, h;
+    A.load(p.A + (int64_t)at.c * p.S, s0, p.S);
+    A.scale(kLog2e);
+    const int64_t chunk_row = ((int64_t)at.n * p.chunks + chunk) * p.channels + at.c;
+    if (ENDS)
+        h.fill(0.f);
+    else if (p.chunks > 1)
+        h.load(p.h_chunk + chunk_row * p.S, s0, p.S);
     else if (p.state)
-        load_states<SPT>(h, p.state + row * p.S, s0, p.S);
+        h.load(p.state + row * p.S, s0, p.S);
     else
-#pragma unroll
-        for (int i = 0; i < SPT; ++i) h[i] = 0.f;
+        h.fill(0.f);
 
     Run<T> u, d, z, un, dn, zn;
-    ScanBC<T, SPT, VE> next;
+    ScanBC<T, SPT, VE, ENDS> next;
     auto fetch = [&](int t0) {
         load_run(un, ur, t0 + j * VE, row_end, p.vec);
         load_run(dn, dr, t0 + j * VE, row_end, p.vec);
-        if (zr) load_run(zn, zr, t0 + j * VE, row_end, p.vec);
+        if (!ENDS && zr) load_run(zn, zr, t0 + j * VE, row_end, p.vec);
         next.load(p, at, t0, end);
     };
+    float total = 0.f;
     if (first < end) fetch(first);
     int buf = 0;
     for (int t0 = first; t0 < end; t0 += TT, buf ^= 1) {
-        float *tile = bc + buf * (2 * TT * SP);
+        float *tile = bc + buf * kBuf;
         next.store(tile);
         u = un; d = dn; z = zn;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             const float dt = t0 + j * VE + e < row_end ? step_size(p, to_f32(d.e[e]) + bias) : 0.f;
-            dtu[j * VE + e] = make_float2(dt, dt * to_f32(u.e[e]));
+            const float du = dt * to_f32(u.e[e]);
+            if (ENDS) total += dt;
+            steps[j * (VE + 1) + e] = make_ulonglong2(pack2(dt, dt), pack2(du, du));
         }
         // one barrier per tile: the other buffer of B and C was last read before
         // the previous one
@@ -81,32 +99,62 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanParams p) 
             float yp[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 x = dtu[t + k];
-                float b[SPT], c[SPT];
-                read_states<SPT>(b, tile + (t + k) * SP + s0);
-                read_states<SPT>(c, tile + (TT + t + k) * SP + s0);
-                yp[k] = 0.f;
+                const ulonglong2 x = steps[t + t / VE + k];
+                Pairs<SPT> b;
+                b.read(tile + (t + k) * SP + s0);
+                f32x2 y = 0;
+                if (ENDS) {
 #pragma unroll
-                for (int i = 0; i < SPT; ++i) {
-                    h[i] = fmaf(ex2(x.x * A[i]), h[i], x.y * b[i]);
-                    yp[k] = fmaf(h[i], c[i], yp[k]);
+                    for (int i = 0; i < NP; ++i)
+                        h.v[i] = fma2(ex2_2(mul2(x.x, A.v[i])), h.v[i], mul2(x.y, b.v[i]));
+                } else {
+                    Pairs<SPT> c;
+                    c.read(tile + (TT + t + k) * SP + s0);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        h.v[i] = fma2(ex2_2(mul2(x.x, A.v[i])), h.v[i], mul2(x.y, b.v[i]));
+                        y = i ? fma2(h.v[i], c.v[i], y) : mul2(h.v[i], c.v[i]);
+                    }
+                }
+                const float2 f = unpack2(y);
+                yp[k] = f.x + f.y;
+            }
+            if (!ENDS)
+                *reinterpret_cast<float4 *>(parts + threadIdx.x * kPartPitch + t) =
+                    make_float4(yp[0], yp[1], yp[2], yp[3]);
+        }
+        __syncwarp();
+        if (!ENDS) {
+            float y[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) y[e] = D * to_f32(u.e[e]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 *q = reinterpret_cast<const float4 *>(
+                    parts + ((threadIdx.x & ~3) + k) * kPartPitch + j * VE);
+#pragma unroll
+                for (int e = 0; e < VE; e += 4) {
+                    const float4 f = q[e / 4];
+                    y[e] += f.x; y[e + 1] += f.y; y[e + 2] += f.z; y[e + 3] += f.w;
                 }
             }
-            *reinterpret_cast<float4 *>(part + lane * (TT + 4) + t) =
-                make_float4(yp[0], yp[1], yp[2], yp[3]);
-        }
-        __syncwarp();
-        Run<T> out;
+            Run<T> out;
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            float y = D * to_f32(u.e[e]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y += part[(ch * 4 + k) * (TT + 4) + j * VE + e];
-            if (zr) y *= silu(to_f32(z.e[e]));
-            out.e[e] = from_f32<T>(t0 + j * VE + e < end ? y : 0.f);
+            for (int e = 0; e < VE; ++e) {
+                if (zr) y[e] *= silu(to_f32(z.e[e]));
+                out.e[e] = from_f32<T>(t0 + j * VE + e < end ? y[e] : 0.f);
+            }
+            if (at.valid) store_run(out, yr, t0 + j * VE, stop, p.vec_y);
+            __syncwarp();
         }
-        if (at.valid) store_run(out, yr, t0 + j * VE, stop, p.vec_y);
-        __syncwarp();
+    }
+    if (ENDS) {
+        total += __shfl_xor_sync(~0u, total, 1);
+        total += __shfl_xor_sync(~0u, total, 2);
+        if (!at.valid) return;
+        h.store(p.h_chunk + chunk_row * p.S, s0, p.S);
+        if (j == 0) p.dt_chunk[chunk_row] = total;
+        return;
     }
     // positions of the chunk behind the last tile
     if (at.valid) {
@@ -115,8 +163,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanParams p) 
 #pragma unroll
         for (int e = 0; e < VE; ++e) zero.e[e] = from_f32<T>(0.f);
         for (int t = done + j * VE; t < stop; t += TT) store_run(zero, yr, t, stop, p.vec_y);
-        if (p.final_state && chunk == p.chunks - 1)
-            store_states<SPT>(p.final_state + row * p.S, h, s0, p.S);
+        if (p.final_state && chunk == p.chunks - 1) h.store(p.final_state + row * p.S, s0, p.S);
     }
 }
 
@@ -124,6 +171,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanParams p) 
 // chunk leaves from a zero state (and g_chunk the gradient that reaches its
 // start from its own outputs), on return the state that it starts from (the
 // gradient of the state that it leaves).  A chunk's decay is e^(A sum dt).
+// Eight chunks are read at a time, so that the reads do not wait for the
+// writes before them.
 __global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, int grad) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t per = (int64_t)p.channels * p.S;
@@ -131,24 +180,34 @@ __global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, in
     const int n = (int)(i / per);
     const int64_t cs = i - n * per;
     const float A = p.A[cs] * kLog2e;
-    const int c = (int)(cs / p.S);
     const int64_t base = (int64_t)n * p.chunks;
-    float h = p.state ? p.state[i] : 0.f;
-    for (int k = 0; k < p.chunks; ++k) {
-        float *at = p.h_chunk + (base + k) * per + cs;
-        const float left = *at;
-        *at = h;
-        h = fmaf(ex2(A * p.dt_chunk[(base + k) * p.channels + c]), h, left);
+    const float *dts = p.dt_chunk + base * p.channels + cs / p.S;
+    constexpr int kBatch = 8;
+    for (int back = 0; back <= grad; ++back) {
+        float *rows = (back ? p.g_chunk : p.h_chunk) + base * per + cs;
+        const float *first = back ? p.dfinal : p.state;
+        float v = first ? first[i] : 0.f;
+        for (int k0 = 0; k0 < p.chunks; k0 += kBatch) {
+            float left[kBatch], decay[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int k = back ? p.chunks - 1 - k0 - e : k0 + e;
+                if (k0 + e < p.chunks) {
+                    left[e] = rows[k * per];
+                    decay[e] = dts[(int64_t)k * p.channels];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+                const int k = back ? p.chunks - 1 - k0 - e : k0 + e;
+                if (k0 + e < p.chunks) {
+                    rows[k * per] = v;
+                    v = fmaf(ex2(A * decay[e]), v, left[e]);
+                }
+            }
+        }
+        if (back && p.dstate) p.dstate[i] = v;
     }
-    if (!grad) return;
-    float g = p.dfinal ? p.dfinal[i] : 0.f;
-    for (int k = p.chunks - 1; k >= 0; --k) {
-        float *at = p.g_chunk + (base + k) * per + cs;
-        const float left = *at;
-        *at = g;
-        g = fmaf(ex2(A * p.dt_chunk[(base + k) * p.channels + c]), g, left);
-    }
-    if (p.dstate) p.dstate[i] = g;
 }
 
 // Step: four lanes per request and channel, as in the scan; the states are
@@ -272,9 +331,37 @@ bool elements(size_t e, std::initializer_list<const void *> ps) {
 
 }  // namespace
 
+namespace {
+
+// Chunks of the forward scan.  One pass over a sequence needs a block per 32
+// channels of each sequence; where that leaves fewer than two blocks per SM,
+// the sequence is cut so that there are four, into chunks of four tiles at least.
+// Two more passes over the states are the price: what every chunk leaves from
+// zero (no outputs), and the join.
+void plan_chunks(ScanParams &p) {
+    const int64_t blocks = (int64_t)p.groups * p.blocks_per_group * p.N;
+    const int64_t tiles = ((int64_t)p.L + kTile - 1) / kTile;
+    p.chunks = 1;
+    p.chunk_len = p.L;
+    if (blocks >= 2 * kSMs || tiles < 8) return;
+    int64_t want = (4 * kSMs + blocks - 1) / blocks;
+    if (want > tiles / 4) want = tiles / 4;
+    const int64_t per = (tiles + want - 1) / want;
+    p.chunk_len = (int)(per * kTile);
+    p.chunks = (int)((tiles + per - 1) / per);
+}
+
+int64_t state_floats(const ScanParams &p) {
+    return ((int64_t)p.N * p.chunks * p.channels * p.S + 3) / 4 * 4;
+}
+
+}  // namespace
+
 SPCONV_API int64_t spconv_scan_workspace(const spconv_scan_args *a) {
-    (void)a;
-    return 0;
+    if (scan_check_sizes(a) || a->channels == 0 || a->N == 0) return 0;
+    ScanParams p = scan_params(a);
+    plan_chunks(p);
+    return p.chunks == 1 ? 0 : (state_floats(p) + (int64_t)p.N * p.chunks * p.channels) * 4;
 }
 
 SPCONV_API int spconv_scan(const spconv_scan_args *a, void *stream) {
@@ -303,16 +390,30 @@ SPCONV_API int spconv_scan(const spconv_scan_args *a, void *stream) {
     if (overlap(a->y, yb, a->final_state, sb) || overlap(a->state, sb, a->final_state, sb))
         return SPCONV_ERR_INVALID_ARG;
     ScanParams p = scan_params(a);
+    plan_chunks(p);
+    if (p.chunks > 1) {
+        const int64_t need = spconv_scan_workspace(a);
+        if (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need)
+            return SPCONV_ERR_INVALID_ARG;
+        p.h_chunk = static_cast<float *>(a->workspace);
+        p.dt_chunk = p.h_chunk + state_floats(p);
+    }
     p.vec_y = rows_aligned(a->y, 0, L, e);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return by_dtype(a->dtype, [&](auto t) {
         return by_states(a->S, [&](auto k) {
-            constexpr int SPT = decltype(k)::value, TT = 32;
-            auto *fn = scan_kernel<decltype(t), SPT>;
-            const size_t smem = sizeof(float) * (4 * TT * 4 * SPT + 4 * (8 * (TT + 2) * 2 + 32 * (TT + 4)));
-            if (int rc = raise_smem(fn, smem)) return rc;
+            using T = decltype(t);
+            constexpr int SPT = decltype(k)::value;
+            constexpr size_t ends = scan_smem<SPT, true>() * 4, full = scan_smem<SPT, false>() * 4;
             const dim3 grid(p.groups * p.blocks_per_group, p.N, p.chunks);
-            fn<<<grid, kScanThreads, smem, s>>>(p);
+            if (p.chunks > 1) {
+                if (int rc = raise_smem(scan_kernel<T, SPT, true>, ends)) return rc;
+                scan_kernel<T, SPT, true><<<grid, kScanThreads, ends, s>>>(p);
+                if (int rc = launch_status()) return rc;
+                if (int rc = scan_join_chunks(p, false, s)) return rc;
+            }
+            if (int rc = raise_smem(scan_kernel<T, SPT, false>, full)) return rc;
+            scan_kernel<T, SPT, false><<<grid, kScanThreads, full, s>>>(p);
             return launch_status();
         });
     });

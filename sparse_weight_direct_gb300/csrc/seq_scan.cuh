@@ -62,10 +62,11 @@ static __device__ __forceinline__ float step_size(const ScanParams &p, float raw
 }
 
 // B and C of one tile: a thread holds VE positions of NB (matrix, state) pairs.
-template <typename T, int SPT, int VE>
+// ONLY_B: without C.
+template <typename T, int SPT, int VE, bool ONLY_B = false>
 struct ScanBC {
     static constexpr int SP = 4 * SPT, TT = 4 * VE;
-    static constexpr int kItems = 2 * SP * 4;
+    static constexpr int kItems = (ONLY_B ? 1 : 2) * SP * 4;
     static constexpr int NB = (kItems + kScanThreads - 1) / kScanThreads;
     Run<T, VE> r[NB];
 
@@ -92,6 +93,76 @@ struct ScanBC {
 #pragma unroll
             for (int e = 0; e < VE; ++e) d[e * SP] = to_f32(r[k].e[e]);
         }
+    }
+};
+
+// The lane's SPT states as pairs; one state (S <= 4) leaves the second half
+// of its pair at zero.
+template <int SPT>
+struct Pairs {
+    static constexpr int N = SPT > 1 ? SPT / 2 : 1;
+    f32x2 v[N];
+
+    // from a row of floats in shared memory
+    __device__ __forceinline__ void read(const float *row) {
+        if constexpr (SPT % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(row + 2 * i);
+                v[i] = q.x;
+                v[i + 1] = q.y;
+            }
+        } else if constexpr (SPT == 2) {
+            v[0] = *reinterpret_cast<const f32x2 *>(row);
+        } else {
+            v[0] = pack2(row[0], 0.f);
+        }
+    }
+    __device__ __forceinline__ void write(float *row) const {
+        if constexpr (SPT % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2)
+                *reinterpret_cast<ulonglong2 *>(row + 2 * i) = make_ulonglong2(v[i], v[i + 1]);
+        } else if constexpr (SPT == 2) {
+            *reinterpret_cast<f32x2 *>(row) = v[0];
+        } else {
+            row[0] = unpack2(v[0]).x;
+        }
+    }
+    // from a row of S floats in global memory, the lane's from s0; zeros behind S
+    __device__ __forceinline__ void load(const float *row, int s0, int S) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int s = s0 + 2 * i;
+            v[i] = pack2(s < S ? row[s] : 0.f, SPT > 1 && s + 1 < S ? row[s + 1] : 0.f);
+        }
+    }
+    __device__ __forceinline__ void store(float *row, int s0, int S) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int s = s0 + 2 * i;
+            const float2 f = unpack2(v[i]);
+            if (s < S) row[s] = f.x;
+            if (SPT > 1 && s + 1 < S) row[s + 1] = f.y;
+        }
+    }
+    __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = pack2(x, x);
+    }
+    __device__ __forceinline__ void scale(float x) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = mul2(v[i], pack2(x, x));
+    }
+    // the sum of all
+    __device__ __forceinline__ float sum() const {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 f = unpack2(v[i]);
+            t += SPT > 1 ? f.x + f.y : f.x;
+        }
+        return t;
     }
 };
 
