@@ -40,11 +40,53 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// V consecutive elements of a row as raw 16-byte words (V * sizeof(T) is a
-// multiple of 16) or, for short runs, as elements.
+// Two elements as they lie in one word, and back (rounded to nearest).
+template <typename T>
+static __device__ __forceinline__ float2 word_to_f32(uint32_t w) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <typename T>
+static __device__ __forceinline__ uint32_t f32_to_word(float a, float b) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+static __device__ __forceinline__ uint32_t bits_of(float v) { return __float_as_uint(v); }
+static __device__ __forceinline__ uint32_t bits_of(__nv_bfloat16 v) {
+    return __bfloat16_as_ushort(v);
+}
+static __device__ __forceinline__ uint32_t bits_of(__half v) { return __half_as_ushort(v); }
+
+// V consecutive elements of a row, kept as the words they are loaded in (as
+// elements, a 16-bit type would take a register each).
 template <typename T, int V = kVec>
 struct alignas(V * sizeof(T) >= 16 ? 16 : V * sizeof(T)) Run {
-    T e[V];
+    static constexpr bool kWide = sizeof(T) == 4;
+    static constexpr int W = V * sizeof(T) / 4;
+    uint32_t w[W];
+
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (kWide) return __uint_as_float(w[i]);
+        else return i & 1 ? word_to_f32<T>(w[i / 2]).y : word_to_f32<T>(w[i / 2]).x;
+    }
+    __device__ __forceinline__ void put(const float (&v)[V]) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            if constexpr (kWide) w[i] = __float_as_uint(v[i]);
+            else w[i] = f32_to_word<T>(v[2 * i], v[2 * i + 1]);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
 };
 
 // row[t0, t0 + V) where t < end, zeros behind (positions behind `end` are not
@@ -54,10 +96,19 @@ template <typename T, int V>
 static __device__ __forceinline__ void load_run(Run<T, V> &r, const T *__restrict__ row, int t0,
                                                 int end, bool vec) {
     if (vec && t0 + V <= end) {
-        r = *reinterpret_cast<const Run<T, V> *>(row + t0);
+        // the rest of the line is the row's next run: have it brought to L2 with this one
+        if constexpr (sizeof(r) == 16)
+            asm("ld.global.nc.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
+                : "l"(row + t0));
+        else
+            r = *reinterpret_cast<const Run<T, V> *>(row + t0);
     } else {
+        r.clear();
+        constexpr int per = 4 / sizeof(T);
 #pragma unroll
-        for (int i = 0; i < V; ++i) r.e[i] = t0 + i < end ? row[t0 + i] : from_f32<T>(0.f);
+        for (int i = 0; i < V; ++i)
+            if (t0 + i < end) r.w[i / per] |= bits_of(row[t0 + i]) << (i % per * 16);
     }
 }
 
@@ -68,9 +119,12 @@ static __device__ __forceinline__ void store_run(const Run<T, V> &r, T *__restri
     if (vec && t0 + V <= L) {
         *reinterpret_cast<Run<T, V> *>(row + t0) = r;
     } else {
+        using Bits = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+        constexpr int per = 4 / sizeof(T);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (t0 + i < L) row[t0 + i] = r.e[i];
+            if (t0 + i < L)
+                reinterpret_cast<Bits *>(row)[t0 + i] = (Bits)(r.w[i / per] >> (i % per * 16));
     }
 }
 
@@ -85,10 +139,15 @@ static __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// 1 / (1 + e^-v)
-static __device__ __forceinline__ float sigmoid(float v) {
-    return __fdividef(1.f, 1.f + __expf(-v));
+// 1 / x, relative error about 2^-23; 0 for an infinite x.
+static __device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+
+// 1 / (1 + e^-v)
+static __device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-kLog2e * v)); }
 static __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 // d silu / dv
 static __device__ __forceinline__ float silu_grad(float v) {
@@ -101,12 +160,12 @@ static __device__ __forceinline__ float silu_grad(float v) {
 // error 4e-9), so the small values that step sizes are keep their digits.
 static __device__ __forceinline__ float softplus(float v) {
     const float e = ex2(-kLog2e * fabsf(v));
-    const float t = __fdividef(e, 2.f + e), x = t * t;
+    const float t = e * rcp(2.f + e), x = t * t;
     float q = fmaf(x, 0.28157778f, 0.27965158f);
     q = fmaf(x, q, 0.40024595f);
     q = fmaf(x, q, 0.66666322f);
     q = fmaf(x, q, 2.00000001f);
-    return fmaxf(v, 0.f) + t * q;
+    return fmaf(t, q, fmaxf(v, 0.f));
 }
 
 // ---------------------------------------------------------------- pairs of floats

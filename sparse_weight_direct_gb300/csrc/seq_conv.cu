@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p) {
     if (run < p.runs) {
         const int t0 = run * kVec;
         Run<T> out;
+        out.clear();
         if (t0 < len) {
             float w[K];
 #pragma unroll
@@ -80,18 +81,17 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p) {
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) s[j] = h[j];
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) s[K - 1 + i] = to_f32(in.e[i]);
+            for (int i = 0; i < kVec; ++i) s[K - 1 + i] = in[i];
+            float o[kVec];
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 float v = b;
 #pragma unroll
                 for (int k = 0; k < K; ++k) v = fmaf(w[k], s[i + k], v);
                 if (p.silu) v = silu(v);
-                out.e[i] = from_f32<T>(t0 + i < len ? v : 0.f);
+                o[i] = t0 + i < len ? v : 0.f;
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) out.e[i] = from_f32<T>(0.f);
+            out.put(o);
         }
         store_run(out, static_cast<T *>(p.y) + rowi * p.L, t0, p.L, p.vec_y);
     }
@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParam
             for (int j = 0; j < K - 1; ++j) s[j] = h[j];
 #pragma unroll
             for (int j = 0; j < kVec; ++j) {
-                s[K - 1 + j] = to_f32(in.e[j]);
-                g[j] = to_f32(gin.e[j]);
+                s[K - 1 + j] = in[j];
+                g[j] = gin[j];
             }
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParam
 #pragma unroll
             for (int j = 0; j < kG; ++j) g[j] = 0.f;
         }
-        Run<T> out;
+        float o[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
             float d = 0.f;
@@ -178,8 +178,10 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParam
             for (int k = 0; k < K; ++k) d = fmaf(w[k], g[j + K - 1 - k], d);
             const int t = t0 + j, back = t - (len - (K - 1));
             if (df && t < len && back >= 0) d += to_f32(df[back]);
-            out.e[j] = from_f32<T>(t < len ? d : 0.f);
+            o[j] = t < len ? d : 0.f;
         }
+        Run<T> out;
+        out.put(o);
         store_run(out, static_cast<T *>(p.dx) + rowi * p.L, t0, p.L, p.vec_y);
         if (K > 1 && p.dstate && run == 0) {
             T *ds = static_cast<T *>(p.dstate) + rowi * (K - 1);

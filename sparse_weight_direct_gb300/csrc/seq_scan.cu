@@ -15,155 +15,277 @@ namespace spconv {
 namespace seq {
 namespace {
 
-// Shared memory of a block, in floats: B and C of two tiles, each channel's
-// {dt, dt, dt u, dt u} and each lane's part of its positions' outputs.
-constexpr int kTile = 4 * kVec;
-constexpr int kStepPitch = kTile + 5;  // rows of 16 bytes: odd, so that eight channels' reads
-                                       // of one position meet no bank twice
-constexpr int kPartPitch = kTile + 4;
-template <int SPT, bool ENDS>
-constexpr int scan_smem() {
-    return (ENDS ? 2 : 4) * kTile * 4 * SPT + kScanChannels * 4 * kStepPitch +
-           (ENDS ? 0 : kScanThreads * kPartPitch);
-}
+// Tiling.  A lane holds SPT states of each of two channels, LPC lanes hold a
+// channel, so a position's 2 * SPT values of B and C, read from shared memory,
+// serve two channels, and its step sizes, two per channel, SPT states.  A
+// broadcast read costs a 4-byte word per lane like any other, and a lane's
+// 2 * (2 * SPT) + 4 words per 2 * SPT updates are what shared memory can deliver
+// about as fast as the exponentials (32 a clock on an SM) can use them: one channel
+// and four states per lane read 2.5 words per update and took 375 us on 4 x
+// 4096 channels x 2048 positions x 16 states in bf16.
+// A block is one warp: its 64 / LPC channels give as many blocks as there are.
+template <typename T, int SPT_, int LPC_>
+struct ScanTile {
+    static constexpr int SPT = SPT_, LPC = LPC_, SP = SPT * LPC;
+    static constexpr int VE = 16 / sizeof(T), TT = 4 * VE;  // positions of a lane's load, of a tile
+    static constexpr int PAIRS = 32 / LPC, CW = 2 * PAIRS;  // pairs of channels, channels
+    static constexpr int NI = CW * 4 / 32;                  // loads of a lane from each row set
+    static constexpr int NB = 2 * SP * 4 / 32;              // from B and C
+    // in rows of 16 bytes {dt, dt u} of a pair's channels: one more after every
+    // VE positions, and odd, so that neither the lanes that write nor the pairs
+    // that read meet in few banks
+    static constexpr int kStepPitch = TT + 5;
+    static constexpr int kOutPitch = TT + 4;
+    static constexpr int kOutHalf = PAIRS * kOutPitch + 16;  // from the pairs' first channels to
+                                                             // their second
+    static constexpr int kSteps = PAIRS * kStepPitch * 4;    // floats
+    // rows of B and of C: one more after every VE positions here too, and one
+    // that is read ahead
+    static constexpr int kMatrix = (TT + 5) * SP;
+    static constexpr int kBC = 2 * kMatrix;
+    static constexpr int kOut = 2 * kOutHalf;
+    static constexpr bool kAhead = NB <= 4;  // B and C of the next tile wait in registers
+};
 
 // One pass over a chunk of positions with the states in registers.
 // ENDS: from zero states, only what the chunk leaves and the sum of its step
-// sizes.  Otherwise the outputs: the y of a position is the sum of the four
-// lanes' parts, joined through shared memory once per tile.
-template <typename T, int SPT, bool ENDS>
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(const ScanParams p) {
-    constexpr int VE = kVec, TT = kTile, SP = 4 * SPT, NP = Pairs<SPT>::N;
-    extern __shared__ __align__(16) float sm[];
-    constexpr int kBuf = (ENDS ? 1 : 2) * TT * SP;
-    float *bc = sm;                                   // [2 buffers][B, C][TT][SP]
-    const int lane = threadIdx.x & 31, j = lane & 3;
-    ulonglong2 *steps = reinterpret_cast<ulonglong2 *>(sm + 2 * kBuf) +
-                        (threadIdx.x >> 2) * kStepPitch;
-    float *parts = sm + 2 * kBuf + kScanChannels * 4 * kStepPitch;
+// sizes.  Otherwise the outputs.
+template <typename T, int SPT, int LPC, bool ENDS>
+__global__ void __launch_bounds__(32) scan_kernel(const ScanParams p) {
+    using G = ScanTile<T, SPT, LPC>;
+    constexpr int VE = G::VE, TT = G::TT, SP = G::SP, NP = Pairs<SPT>::N, NI = G::NI, NB = G::NB;
+    __shared__ __align__(16) float steps[G::kSteps];
+    __shared__ __align__(16) float bc[G::kBC];       // [B, C][row of TT + 5][SP]
+    __shared__ __align__(16) float outs[ENDS ? 4 : G::kOut];
+    const int lane = threadIdx.x;
+    // as owner of states: pair of channels, lane of the pair
+    const int pair = lane / LPC, j = lane % LPC, s0 = j * SPT;
+    // as owner of positions: VE * quarter .. of channels lane / 4 + 8 k
+    const int quarter = lane & 3, t_mine = quarter * VE;
 
-    const int cb = blockIdx.x, chunk = blockIdx.z;
-    const ScanPlace at(p, blockIdx.y, cb);
+    const int n = blockIdx.y, chunk = blockIdx.z;
+    const int g = blockIdx.x / p.blocks_per_group;
+    const int c_first = (blockIdx.x - g * p.blocks_per_group) * G::CW;  // within the group
+    const int c_count = min(G::CW, p.per_group - c_first);
+    const int64_t c_base = (int64_t)g * p.per_group + c_first;
+    const int len = p.lengths ? min(max(p.lengths[n], 0), p.L) : p.L;
     const int first = chunk * p.chunk_len, stop = first + min(p.L - first, p.chunk_len);
-    const int end = max(min(at.len, stop), first), row_end = at.valid ? end : 0;
-    const int64_t row = (int64_t)at.n * p.channels + at.c;
-    const T *ur = static_cast<const T *>(p.u) + at.n * p.u_sn + at.c * p.u_sc;
-    const T *dr = static_cast<const T *>(p.delta) + at.n * p.d_sn + at.c * p.d_sc;
-    const T *zr = !ENDS && p.z ? static_cast<const T *>(p.z) + at.n * p.z_sn + at.c * p.z_sc
+    const int end = max(min(len, stop), first);
+    const int64_t rows = (int64_t)n * p.channels + c_base;
+    const int64_t chunk_rows = ((int64_t)n * p.chunks + chunk) * p.channels + c_base;
+    const T *ub = static_cast<const T *>(p.u) + n * p.u_sn + c_base * p.u_sc;
+    const T *db = static_cast<const T *>(p.delta) + n * p.d_sn + c_base * p.d_sc;
+    const T *zb = !ENDS && p.z ? static_cast<const T *>(p.z) + n * p.z_sn + c_base * p.z_sc
                                : nullptr;
-    T *yr = static_cast<T *>(p.y) + row * p.L;
-    const float bias = p.delta_bias ? p.delta_bias[at.c] : 0.f, D = p.D ? p.D[at.c] : 0.f;
-    const int s0 = j * SPT;
+    const T *Bb = static_cast<const T *>(p.B) + n * p.b_sn + g * p.b_sg;
+    const T *Cb = static_cast<const T *>(p.C) + n * p.c_sn + g * p.c_sg;
 
-    Pairs<SPT> A, h;
-    A.load(p.A + (int64_t)at.c * p.S, s0, p.S);
-    A.scale(kLog2e);
-    const int64_t chunk_row = ((int64_t)at.n * p.chunks + chunk) * p.channels + at.c;
-    if (ENDS)
-        h.fill(0.f);
-    else if (p.chunks > 1)
-        h.load(p.h_chunk + chunk_row * p.S, s0, p.S);
-    else if (p.state)
-        h.load(p.state + row * p.S, s0, p.S);
-    else
-        h.fill(0.f);
+    Pairs<SPT> A[2], h[2];
+    int mine[2];  // the pair's channels in the block
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        mine[k] = pair + k * G::PAIRS;
+        const int S = mine[k] < c_count ? p.S : 0;
+        A[k].load(p.A + (c_base + mine[k]) * p.S, s0, S);
+        A[k].scale(kLog2e);
+        if (ENDS)
+            h[k].fill(0.f);
+        else if (p.chunks > 1)
+            h[k].load(p.h_chunk + (chunk_rows + mine[k]) * p.S, s0, S);
+        else if (p.state)
+            h[k].load(p.state + (rows + mine[k]) * p.S, s0, S);
+        else
+            h[k].fill(0.f);
+    }
+    float bias[NI], D[NI], total[NI];
+    int row_end[NI];
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+        const int c = lane / 4 + 8 * k;
+        row_end[k] = c < c_count ? end : 0;
+        bias[k] = p.delta_bias && c < c_count ? p.delta_bias[c_base + c] : 0.f;
+        D[k] = p.D && c < c_count ? p.D[c_base + c] : 0.f;
+        total[k] = 0.f;
+    }
 
-    Run<T> u, d, z, un, dn, zn;
-    ScanBC<T, SPT, VE, ENDS> next;
-    auto fetch = [&](int t0) {
-        load_run(un, ur, t0 + j * VE, row_end, p.vec);
-        load_run(dn, dr, t0 + j * VE, row_end, p.vec);
-        if (!ENDS && zr) load_run(zn, zr, t0 + j * VE, row_end, p.vec);
-        next.load(p, at, t0, end);
+    Run<T, VE> u[NI], un[NI], dn[NI], z[NI], bcn[NB];
+    auto fetch_bc = [&](int t0) {
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const int i = lane + 32 * k, s = i % SP, q = (i / SP) % 4, which = i / (SP * 4);
+            if (ENDS && which) continue;
+            const T *row = which ? Cb + s * p.c_ss : Bb + s * p.b_ss;
+            load_run(bcn[k], row, t0 + q * VE, s < p.S ? end : 0, p.vec);
+        }
     };
-    float total = 0.f;
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            const int c = lane / 4 + 8 * k;
+            load_run(dn[k], db + c * p.d_sc, t0 + t_mine, row_end[k], p.vec);
+            load_run(un[k], ub + c * p.u_sc, t0 + t_mine, row_end[k], p.vec);
+        }
+        if (G::kAhead) fetch_bc(t0);
+    };
     if (first < end) fetch(first);
-    int buf = 0;
-    for (int t0 = first; t0 < end; t0 += TT, buf ^= 1) {
-        float *tile = bc + buf * kBuf;
-        next.store(tile);
-        u = un; d = dn; z = zn;
+    for (int t0 = first; t0 < end; t0 += TT) {
+        if (!G::kAhead) fetch_bc(t0);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            const float dt = t0 + j * VE + e < row_end ? step_size(p, to_f32(d.e[e]) + bias) : 0.f;
-            const float du = dt * to_f32(u.e[e]);
-            if (ENDS) total += dt;
-            steps[j * (VE + 1) + e] = make_ulonglong2(pack2(dt, dt), pack2(du, du));
+        for (int k = 0; k < NB; ++k) {
+            const int i = lane + 32 * k, s = i % SP, q = (i / SP) % 4, which = i / (SP * 4);
+            if (ENDS && which) continue;
+            float *to = bc + which * G::kMatrix + q * (VE + 1) * SP + s;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) to[e * SP] = bcn[k][e];
         }
-        // one barrier per tile: the other buffer of B and C was last read before
-        // the previous one
-        __syncthreads();
-        if (t0 + TT < end) fetch(t0 + TT);
-#pragma unroll 2
-        for (int t = 0; t < TT; t += 4) {
-            float yp[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const ulonglong2 x = steps[t + t / VE + k];
-                Pairs<SPT> b;
-                b.read(tile + (t + k) * SP + s0);
-                f32x2 y = 0;
-                if (ENDS) {
+        for (int k = 0; k < NI; ++k) {
+            const int c = lane / 4 + 8 * k;
+            float2 *to = reinterpret_cast<float2 *>(steps) +
+                         ((c % G::PAIRS) * G::kStepPitch + quarter * (VE + 1)) * 2 + c / G::PAIRS;
+            u[k] = un[k];
+            float dt[VE];
 #pragma unroll
-                    for (int i = 0; i < NP; ++i)
-                        h.v[i] = fma2(ex2_2(mul2(x.x, A.v[i])), h.v[i], mul2(x.y, b.v[i]));
-                } else {
-                    Pairs<SPT> c;
-                    c.read(tile + (TT + t + k) * SP + s0);
+            for (int e = 0; e < VE; ++e) dt[e] = dn[k][e] + bias[k];
+            if (p.softplus) {
 #pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        h.v[i] = fma2(ex2_2(mul2(x.x, A.v[i])), h.v[i], mul2(x.y, b.v[i]));
-                        y = i ? fma2(h.v[i], c.v[i], y) : mul2(h.v[i], c.v[i]);
-                    }
-                }
-                const float2 f = unpack2(y);
-                yp[k] = f.x + f.y;
+                for (int e = 0; e < VE; ++e) dt[e] = softplus(dt[e]);
             }
-            if (!ENDS)
-                *reinterpret_cast<float4 *>(parts + threadIdx.x * kPartPitch + t) =
-                    make_float4(yp[0], yp[1], yp[2], yp[3]);
-        }
-        __syncwarp();
-        if (!ENDS) {
-            float y[VE];
-#pragma unroll
-            for (int e = 0; e < VE; ++e) y[e] = D * to_f32(u.e[e]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 *q = reinterpret_cast<const float4 *>(
-                    parts + ((threadIdx.x & ~3) + k) * kPartPitch + j * VE);
-#pragma unroll
-                for (int e = 0; e < VE; e += 4) {
-                    const float4 f = q[e / 4];
-                    y[e] += f.x; y[e + 1] += f.y; y[e + 2] += f.z; y[e + 3] += f.w;
-                }
-            }
-            Run<T> out;
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                if (zr) y[e] *= silu(to_f32(z.e[e]));
-                out.e[e] = from_f32<T>(t0 + j * VE + e < end ? y[e] : 0.f);
+                to[2 * e] = make_float2(dt[e], dt[e] * u[k][e]);
+                if (ENDS) total[k] += t0 + t_mine + e < row_end[k] ? dt[e] : 0.f;
             }
-            if (at.valid) store_run(out, yr, t0 + j * VE, stop, p.vec_y);
+        }
+        if (t0 + TT > end || c_count < G::CW) {
+            // behind the end a step of size zero leaves the states as they are
             __syncwarp();
+            for (int i = lane; i < G::CW * TT; i += 32) {
+                const int c = i / TT, t = i % TT;
+                if (t0 + t >= end || c >= c_count)
+                    reinterpret_cast<float2 *>(steps)[((c % G::PAIRS) * G::kStepPitch + t + t / VE) * 2 +
+                                                      c / G::PAIRS] = make_float2(0.f, 0.f);
+            }
+        }
+        __syncwarp();
+        if (t0 + TT < end) fetch(t0 + TT);
+        if (!ENDS && zb) {
+#pragma unroll
+            for (int k = 0; k < NI; ++k)
+                load_run(z[k], zb + (lane / 4 + 8 * k) * p.z_sc, t0 + t_mine, row_end[k], p.vec);
+        }
+        const float4 *step = reinterpret_cast<const float4 *>(steps) + pair * G::kStepPitch;
+        // what a position needs is read one position ahead (behind the tile's last
+        // one lie rows that are not used)
+        float4 xn = step[0];
+        Pairs<SPT> bn, cn;
+        bn.read(bc + s0);
+        if (!ENDS) cn.read(bc + G::kMatrix + s0);
+#pragma unroll 1
+        for (int t = 0; t < TT; t += 4) {
+            float out[4][2];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 x = xn;
+                const Pairs<SPT> b = bn, c = cn;
+                const int t1 = t + k + 1;
+                const int r1 = k == 3 ? t1 + t1 / VE : t + t / VE + k + 1;
+                xn = step[r1];
+                bn.read(bc + r1 * SP + s0);
+                if (!ENDS) cn.read(bc + G::kMatrix + r1 * SP + s0);
+                const f32x2 dt[2] = {pack2(x.x, x.x), pack2(x.z, x.z)};
+                const f32x2 du[2] = {pack2(x.y, x.y), pack2(x.w, x.w)};
+                f32x2 a[2][NP], y[2];
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) a[q][i] = ex2_2(mul2(dt[q], A[q].v[i]));
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        h[q].v[i] = fma2(a[q][i], h[q].v[i], mul2(du[q], b.v[i]));
+                        if (!ENDS) y[q] = i ? fma2(h[q].v[i], c.v[i], y[q]) : mul2(h[q].v[i], c.v[i]);
+                    }
+                }
+                if (!ENDS) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float2 f = unpack2(y[q]);
+                        out[k][q] = f.x + f.y;
+                    }
+                }
+            }
+            if (!ENDS) {
+                // even lanes keep the pair's first channel, odd lanes the second
+                float w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = (j & 1 ? out[k][1] : out[k][0]) +
+                           __shfl_xor_sync(~0u, j & 1 ? out[k][0] : out[k][1], 1);
+                if (LPC == 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] += __shfl_xor_sync(~0u, w[k], 2);
+                }
+                if (j < 2)
+                    *reinterpret_cast<float4 *>(outs + j * G::kOutHalf + pair * G::kOutPitch + t) =
+                        make_float4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        __syncwarp();
+        if (ENDS) continue;
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            const int c = lane / 4 + 8 * k;
+            const float4 *q = reinterpret_cast<const float4 *>(
+                outs + c / G::PAIRS * G::kOutHalf + c % G::PAIRS * G::kOutPitch + t_mine);
+            float o[VE];
+#pragma unroll
+            for (int e = 0; e < VE; e += 4) {
+                const float4 f = q[e / 4];
+                const float y[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[e + i] = fmaf(D[k], u[k][e + i], y[i]);
+            }
+            if (zb) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) o[e] *= silu(z[k][e]);
+            }
+            if (t0 + TT > end)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) o[e] = t0 + t_mine + e < end ? o[e] : 0.f;
+            Run<T, VE> out;
+            out.put(o);
+            if (c < c_count)
+                store_run(out, static_cast<T *>(p.y) + (rows + c) * p.L, t0 + t_mine, stop, p.vec_y);
         }
     }
     if (ENDS) {
-        total += __shfl_xor_sync(~0u, total, 1);
-        total += __shfl_xor_sync(~0u, total, 2);
-        if (!at.valid) return;
-        h.store(p.h_chunk + chunk_row * p.S, s0, p.S);
-        if (j == 0) p.dt_chunk[chunk_row] = total;
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            total[k] += __shfl_xor_sync(~0u, total[k], 1);
+            total[k] += __shfl_xor_sync(~0u, total[k], 2);
+            const int c = lane / 4 + 8 * k;
+            if (quarter == 0 && c < c_count) p.dt_chunk[chunk_rows + c] = total[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (mine[k] < c_count) h[k].store(p.h_chunk + (chunk_rows + mine[k]) * p.S, s0, p.S);
         return;
     }
     // positions of the chunk behind the last tile
-    if (at.valid) {
-        const int done = first + (end - first + TT - 1) / TT * TT;
-        Run<T> zero;
+    const int done = first + (end - first + TT - 1) / TT * TT;
+    if (done < stop) {
+        Run<T, VE> zero;
+        zero.clear();
+        for (int c = lane / 4; c < c_count; c += 8)
+            for (int t = done + t_mine; t < stop; t += TT)
+                store_run(zero, static_cast<T *>(p.y) + (rows + c) * p.L, t, stop, p.vec_y);
+    }
+    if (p.final_state && chunk == p.chunks - 1) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) zero.e[e] = from_f32<T>(0.f);
-        for (int t = done + j * VE; t < stop; t += TT) store_run(zero, yr, t, stop, p.vec_y);
-        if (p.final_state && chunk == p.chunks - 1) h.store(p.final_state + row * p.S, s0, p.S);
+        for (int k = 0; k < 2; ++k)
+            if (mine[k] < c_count) h[k].store(p.final_state + (rows + mine[k]) * p.S, s0, p.S);
     }
 }
 
@@ -251,16 +373,6 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
     }
 }
 
-template <typename F>
-int raise_smem(F *fn, size_t bytes) {
-    if (bytes <= 48 * 1024) return SPCONV_OK;
-    return cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)bytes) == cudaSuccess
-               ? SPCONV_OK
-               : SPCONV_ERR_CUDA;
-}
-
 }  // namespace
 
 int scan_check_sizes(const spconv_scan_args *a) {
@@ -333,22 +445,40 @@ bool elements(size_t e, std::initializer_list<const void *> ps) {
 
 namespace {
 
-// Chunks of the forward scan.  One pass over a sequence needs a block per 32
-// channels of each sequence; where that leaves fewer than two blocks per SM,
-// the sequence is cut so that there are four, into chunks of four tiles at least.
-// Two more passes over the states are the price: what every chunk leaves from
-// zero (no outputs), and the join.
+constexpr int64_t kSplitBelow = 304, kSplitTo = 1216;  // warps
+
+// f(SPT, LPC) for the smallest tile that holds S states.
+template <typename F>
+int by_tile(int S, bool wide, F f) {
+    using std::integral_constant;
+    if (S <= 4) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    if (S <= 8) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+    if (S <= 16)
+        return wide ? f(integral_constant<int, 8>{}, integral_constant<int, 2>{})
+                    : f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    if (S <= 32) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+}
+
+// Blocks and chunks of the forward scan.  One pass over a sequence needs a warp
+// per 32 channels of each sequence; where that leaves schedulers idle the
+// sequence is cut, into chunks of 128 positions at least.  Two more
+// passes over the states are the price: what every chunk leaves from zero (no
+// outputs), and the join.
 void plan_chunks(ScanParams &p) {
+    p.wide = (int64_t)p.N * p.channels >= 16 * 4096;
+    const int cw = p.S <= 8 || p.S > 16 && p.S <= 32 || p.S <= 16 && p.wide ? 32 : 16;
+    p.blocks_per_group = (p.per_group + cw - 1) / cw;
     const int64_t blocks = (int64_t)p.groups * p.blocks_per_group * p.N;
-    const int64_t tiles = ((int64_t)p.L + kTile - 1) / kTile;
+    const int64_t most = p.L / 128;
     p.chunks = 1;
     p.chunk_len = p.L;
-    if (blocks >= 2 * kSMs || tiles < 8) return;
-    int64_t want = (4 * kSMs + blocks - 1) / blocks;
-    if (want > tiles / 4) want = tiles / 4;
-    const int64_t per = (tiles + want - 1) / want;
-    p.chunk_len = (int)(per * kTile);
-    p.chunks = (int)((tiles + per - 1) / per);
+    if (blocks >= kSplitBelow || most < 2) return;
+    int64_t want = (kSplitTo + blocks - 1) / blocks;
+    if (want > most) want = most;
+    const int64_t len = ((p.L + want - 1) / want + 31) / 32 * 32;  // whole tiles of either type
+    p.chunk_len = (int)len;
+    p.chunks = (int)((p.L + len - 1) / len);
 }
 
 int64_t state_floats(const ScanParams &p) {
@@ -401,19 +531,16 @@ SPCONV_API int spconv_scan(const spconv_scan_args *a, void *stream) {
     p.vec_y = rows_aligned(a->y, 0, L, e);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return by_dtype(a->dtype, [&](auto t) {
-        return by_states(a->S, [&](auto k) {
+        return by_tile(a->S, p.wide, [&](auto spt, auto lpc) {
             using T = decltype(t);
-            constexpr int SPT = decltype(k)::value;
-            constexpr size_t ends = scan_smem<SPT, true>() * 4, full = scan_smem<SPT, false>() * 4;
+            constexpr int SPT = decltype(spt)::value, LPC = decltype(lpc)::value;
             const dim3 grid(p.groups * p.blocks_per_group, p.N, p.chunks);
             if (p.chunks > 1) {
-                if (int rc = raise_smem(scan_kernel<T, SPT, true>, ends)) return rc;
-                scan_kernel<T, SPT, true><<<grid, kScanThreads, ends, s>>>(p);
+                scan_kernel<T, SPT, LPC, true><<<grid, 32, 0, s>>>(p);
                 if (int rc = launch_status()) return rc;
                 if (int rc = scan_join_chunks(p, false, s)) return rc;
             }
-            if (int rc = raise_smem(scan_kernel<T, SPT, false>, full)) return rc;
-            scan_kernel<T, SPT, false><<<grid, kScanThreads, full, s>>>(p);
+            scan_kernel<T, SPT, LPC, false><<<grid, 32, 0, s>>>(p);
             return launch_status();
         });
     });

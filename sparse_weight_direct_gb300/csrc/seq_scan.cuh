@@ -37,6 +37,7 @@ struct ScanParams {
     int softplus, num_slots;
     int chunks, chunk_len;         // chunk_len: a multiple of the tile
     int segments, chunks_per_segment;
+    int wide;                      // forward: the tile with fewer lanes per channel
     int vec;                       // input rows can be read as vectors
     int vec_y;                     // output rows (N x channels x L) likewise
 };
@@ -91,7 +92,7 @@ struct ScanBC {
             const int s = i % SP, q = (i / SP) % 4, which = i / (SP * 4);
             float *d = to + which * (TT * SP) + q * VE * SP + s;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) d[e * SP] = to_f32(r[k].e[e]);
+            for (int e = 0; e < VE; ++e) d[e * SP] = r[k][e];
         }
     }
 };

@@ -76,10 +76,10 @@ __global__ void __launch_bounds__(kScanThreads) chunk_ends_kernel(const ScanPara
         rows.store(bc);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-            const float dt = t0 + j * VE + e < row_end ? step_size(p, to_f32(d.e[e]) + bias) : 0.f;
-            float o = to_f32(dy.e[e]);
-            if (zr) o *= silu(to_f32(z.e[e]));
-            xs[ch][j * VE + e] = make_float4(dt, dt * to_f32(u.e[e]), o, 0.f);
+            const float dt = t0 + j * VE + e < row_end ? step_size(p, d[e] + bias) : 0.f;
+            float o = dy[e];
+            if (zr) o *= silu(z[e]);
+            xs[ch][j * VE + e] = make_float4(dt, dt * u[e], o, 0.f);
         }
         __syncthreads();
 #pragma unroll 4
@@ -166,12 +166,12 @@ __global__ void __launch_bounds__(kScanThreads) gradient_kernel(const ScanParams
         rows.store(bc);
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-            const float dt = mine + e < row_end ? step_size(p, to_f32(d.e[e]) + bias) : 0.f;
-            float o = to_f32(dy.e[e]);
-            if (zr) o *= silu(to_f32(z.e[e]));
-            dtu[j * VE + e] = make_float2(dt, dt * to_f32(u.e[e]));
+            const float dt = mine + e < row_end ? step_size(p, d[e] + bias) : 0.f;
+            float o = dy[e];
+            if (zr) o *= silu(z[e]);
+            dtu[j * VE + e] = make_float2(dt, dt * u[e]);
             dob[j * VE + e] = o;
-            dD = fmaf(o, to_f32(u.e[e]), dD);
+            dD = fmaf(o, u[e], dD);
         }
         __syncthreads();
         // forwards: h_t of every position, and o without D u
@@ -196,13 +196,14 @@ __global__ void __launch_bounds__(kScanThreads) gradient_kernel(const ScanParams
         __syncthreads();
         // dz, and this block's share of dC
         if (zr) {
-            Run<T, VE> out;
+            float w[VE];
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float o = fmaf(D, to_f32(u.e[e]), yb[j * VE + e]);
-                out.e[e] = from_f32<T>(mine + e < end ? to_f32(dy.e[e]) * o * silu_grad(to_f32(z.e[e]))
-                                                      : 0.f);
+                const float o = fmaf(D, u[e], yb[j * VE + e]);
+                w[e] = mine + e < end ? dy[e] * o * silu_grad(z[e]) : 0.f;
             }
+            Run<T, VE> out;
+            out.put(w);
             if (at.valid) store_run(out, static_cast<T *>(p.dz) + row * p.L, mine, stop, p.vec_y);
         }
         // over = the sum over the block's channels of w(channel, t) * hb[t][channel][s]
@@ -252,19 +253,22 @@ __global__ void __launch_bounds__(kScanThreads) gradient_kernel(const ScanParams
             }
         }
         {
-            Run<T, VE> du, dd;
+            float wu[VE], wd[VE];
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float raw = to_f32(d.e[e]) + bias, uu = to_f32(u.e[e]);
+                const float raw = d[e] + bias, uu = u[e];
                 const float dt = dtu[j * VE + e].x;
                 const bool in = mine + e < end;
                 float ddt = fmaf(sums[0][e], uu, sums[1][e]);
                 if (p.softplus) ddt *= sigmoid(raw);
                 ddt = in ? ddt : 0.f;
                 dbias += at.valid ? ddt : 0.f;
-                dd.e[e] = from_f32<T>(ddt);
-                du.e[e] = from_f32<T>(in ? fmaf(sums[0][e], dt, D * dob[j * VE + e]) : 0.f);
+                wd[e] = ddt;
+                wu[e] = in ? fmaf(sums[0][e], dt, D * dob[j * VE + e]) : 0.f;
             }
+            Run<T, VE> du, dd;
+            du.put(wu);
+            dd.put(wd);
             if (at.valid) {
                 store_run(du, static_cast<T *>(p.du) + row * p.L, mine, stop, p.vec_y);
                 store_run(dd, static_cast<T *>(p.ddelta) + row * p.L, mine, stop, p.vec_y);
