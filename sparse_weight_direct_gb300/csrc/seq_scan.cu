@@ -34,14 +34,14 @@ struct ScanTile {
     // in rows of 16 bytes {dt, dt u} of a pair's channels: one more after every
     // VE positions, and odd, so that neither the lanes that write nor the pairs
     // that read meet in few banks
-    static constexpr int kStepPitch = TT + 5;
+    static constexpr int kStepPitch = TT + 7;
     static constexpr int kOutPitch = TT + 4;
     static constexpr int kOutHalf = PAIRS * kOutPitch + 16;  // from the pairs' first channels to
                                                              // their second
     static constexpr int kSteps = PAIRS * kStepPitch * 4;    // floats
-    // rows of B and of C: one more after every VE positions here too, and one
-    // that is read ahead
-    static constexpr int kMatrix = (TT + 5) * SP;
+    // rows of B and of C: one more after every VE positions here too, and two
+    // that are read ahead
+    static constexpr int kMatrix = (TT + 6) * SP;
     static constexpr int kBC = 2 * kMatrix;
     static constexpr int kOut = 2 * kOutHalf;
     static constexpr bool kAhead = NB <= 4;  // B and C of the next tile wait in registers
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanParams p) {
     using G = ScanTile<T, SPT, LPC>;
     constexpr int VE = G::VE, TT = G::TT, SP = G::SP, NP = Pairs<SPT>::N, NI = G::NI, NB = G::NB;
     __shared__ __align__(16) float steps[G::kSteps];
-    __shared__ __align__(16) float bc[G::kBC];       // [B, C][row of TT + 5][SP]
+    __shared__ __align__(16) float bc[G::kBC];       // [B, C][row of TT + 6][SP]
     __shared__ __align__(16) float outs[ENDS ? 4 : G::kOut];
     const int lane = threadIdx.x;
     // as owner of states: pair of channels, lane of the pair
@@ -175,39 +175,48 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanParams p) {
                 load_run(z[k], zb + (lane / 4 + 8 * k) * p.z_sc, t0 + t_mine, row_end[k], p.vec);
         }
         const float4 *step = reinterpret_cast<const float4 *>(steps) + pair * G::kStepPitch;
-        // what a position needs is read one position ahead (behind the tile's last
-        // one lie rows that are not used)
+        // Two positions ahead of the states, what a position needs is read; one
+        // ahead, its decays and inputs are formed: a warp has few neighbours to
+        // hide a latency behind.  (Behind the tile's last position lie rows that
+        // are read and not used.)
         float4 xn = step[0];
-        Pairs<SPT> bn, cn;
+        Pairs<SPT> bn, cn, c1;
         bn.read(bc + s0);
         if (!ENDS) cn.read(bc + G::kMatrix + s0);
+        f32x2 a1[2][NP], b1[2][NP];
+        auto advance = [&](int r) {  // forms the position that was read, reads row r
+            const f32x2 dt[2] = {pack2(xn.x, xn.x), pack2(xn.z, xn.z)};
+            const f32x2 du[2] = {pack2(xn.y, xn.y), pack2(xn.w, xn.w)};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    a1[q][i] = ex2_2(mul2(dt[q], A[q].v[i]));
+                    b1[q][i] = mul2(du[q], bn.v[i]);
+                }
+            }
+            c1 = cn;
+            xn = step[r];
+            bn.read(bc + r * SP + s0);
+            if (!ENDS) cn.read(bc + G::kMatrix + r * SP + s0);
+        };
+        advance(1);
 #pragma unroll 1
         for (int t = 0; t < TT; t += 4) {
             float out[4][2];
+            const int r0 = t + t / VE, r4 = t + 4 + (t + 4) / VE;  // rows of t and t + 4
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float4 x = xn;
-                const Pairs<SPT> b = bn, c = cn;
-                const int t1 = t + k + 1;
-                const int r1 = k == 3 ? t1 + t1 / VE : t + t / VE + k + 1;
-                xn = step[r1];
-                bn.read(bc + r1 * SP + s0);
-                if (!ENDS) cn.read(bc + G::kMatrix + r1 * SP + s0);
-                const f32x2 dt[2] = {pack2(x.x, x.x), pack2(x.z, x.z)};
-                const f32x2 du[2] = {pack2(x.y, x.y), pack2(x.w, x.w)};
-                f32x2 a[2][NP], y[2];
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) a[q][i] = ex2_2(mul2(dt[q], A[q].v[i]));
+                f32x2 y[2];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        h[q].v[i] = fma2(a[q][i], h[q].v[i], mul2(du[q], b.v[i]));
-                        if (!ENDS) y[q] = i ? fma2(h[q].v[i], c.v[i], y[q]) : mul2(h[q].v[i], c.v[i]);
+                        h[q].v[i] = fma2(a1[q][i], h[q].v[i], b1[q][i]);
+                        if (!ENDS) y[q] = i ? fma2(h[q].v[i], c1.v[i], y[q]) : mul2(h[q].v[i], c1.v[i]);
                     }
                 }
+                advance(k < 2 ? r0 + k + 2 : r4 + k - 2);
                 if (!ENDS) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
