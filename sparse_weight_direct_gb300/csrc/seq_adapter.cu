@@ -2,24 +2,39 @@
 //
 //   out = y + scale_i b_i (a_i x),  i = index[n];  out = y where i is no adapter
 //
-// Two kernels: v = a_i x (R x P floats per request, in the workspace), then the
-// sum over R beside the read of y.
+// Bound: x and y are read once and out written once, and 2 R (C + M)
+// operations per position are few beside that, so memory bounds prompts and
+// latency bounds tokens.  Both forms are one launch: a thread-block cluster
+// takes a tile of one request's positions, its blocks split the C channels of
+// v = a x, add their parts of v through distributed shared memory in the
+// order of their ranks, and split the M rows of b v.  So x is read once, v
+// never leaves the SMs, and the rows of b and y that do not depend on v can be
+// fetched before it is there.
+//
+// Prompts use matrix instructions on registers (mma.sync): with R <= 64 rows
+// an operand tile is far too small to keep the tensor memory path busy, and
+// the products take a fraction of the time of the reads and writes around them.
+#include <cooperative_groups.h>
+
+#include <utility>
+
 #include "seq_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace spconv {
 namespace seq {
 namespace {
-
-constexpr int kThreads = 256;
 
 struct AdapterParams {
     const void *x, *a, *b, *y;
     const int32_t *index;
     const float *scale;
     void *out;
-    float *v;
     int64_t x_sn, x_sc;
     int N, P, C, M, R, adapters;
+    int tiles;                     // prompts: tiles of positions of a request
+    int vec_x, vec_a, vec_b, vec_y;  // rows can be read 16 (b of prompts: 4) bytes at a time
 };
 
 static __device__ __forceinline__ int adapter_of(const AdapterParams &p, int64_t n) {
@@ -27,45 +42,535 @@ static __device__ __forceinline__ int adapter_of(const AdapterParams &p, int64_t
     return i >= 0 && i < p.adapters ? i : -1;
 }
 
+// ---------------------------------------------------------------- matrix instructions
+
+// d += a b, 16 x 8 x 16 of 16-bit types
 template <typename T>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const AdapterParams p) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (int64_t)p.N * p.R * p.P) return;
-    const int64_t nr = i / p.P, n = nr / p.R;
-    const int pos = (int)(i - nr * p.P), r = (int)(nr - n * p.R);
-    const int k = adapter_of(p, n);
-    if (k < 0) return;
-    const T *x = static_cast<const T *>(p.x) + n * p.x_sn + pos;
-    const T *a = static_cast<const T *>(p.a) + ((int64_t)k * p.R + r) * p.C;
-    float v = 0.f;
-    for (int c = 0; c < p.C; ++c) v = fmaf(to_f32(a[c]), to_f32(x[c * p.x_sc]), v);
-    p.v[i] = v;
+static __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d += a b, 16 x 8 x 8 of 32-bit values with 11 bits of significand
+static __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// v = hi + lo, each of 11 bits: 22 of v's 24 bits.  An infinity or NaN is all
+// in hi.
+static __device__ __forceinline__ void split_tf32(float v, uint32_t &hi, uint32_t &lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
+    const float rest = v - __uint_as_float(hi);
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(fabsf(v) <= 3.402e38f ? rest : 0.f));
+}
+// two values as words of 16-bit parts: hi, and what hi leaves
+static __device__ __forceinline__ void split_bf16(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = f32_to_word<__nv_bfloat16>(a, b);
+    const float2 h = word_to_f32<__nv_bfloat16>(hi);
+    lo = f32_to_word<__nv_bfloat16>(fabsf(a) <= 3.38e38f ? a - h.x : 0.f,
+                                    fabsf(b) <= 3.38e38f ? b - h.y : 0.f);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const AdapterParams p) {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (int64_t)p.N * p.M * p.P) return;
-    const int64_t nm = i / p.P, n = nm / p.M;
-    const int pos = (int)(i - nm * p.P), m = (int)(nm - n * p.M);
-    const int k = adapter_of(p, n);
-    float o = to_f32(static_cast<const T *>(p.y)[i]);
-    if (k >= 0) {
-        const T *b = static_cast<const T *>(p.b) + ((int64_t)k * p.M + m) * p.R;
-        const float *v = p.v + n * p.R * p.P + pos;
-        float s = 0.f;
-        for (int r = 0; r < p.R; ++r) s = fmaf(to_f32(b[r]), v[(int64_t)r * p.P], s);
-        o = fmaf(p.scale ? p.scale[k] : 1.f, s, o);
-    }
-    static_cast<T *>(p.out)[i] = from_f32<T>(o);
+static __device__ __forceinline__ uint32_t smem_address(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
+static __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_address(p)));
+}
+static __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_address(p)));
+}
+// 16 bytes, or zeros
+static __device__ __forceinline__ void copy16(void *to, const void *from, bool on) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem_address(to)),
+                 "l"(from), "r"(on ? 16 : 0)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- prompts
+
+constexpr int kPos = 64;    // positions of a tile
+constexpr int kChan = 64;   // channels of a stage
+constexpr int kStages = 3;
+constexpr int kThreads = 128;
+
+template <typename T, int RT>
+struct PromptTile {
+    static constexpr bool kWide = sizeof(T) == 4;
+    static constexpr int RP = 16 * RT;  // rows of a, padded
+    static constexpr int kVec = 16 / sizeof(T);
+    // pitches in elements: the eight rows of a matrix read start in different
+    // banks; 32-bit fragments take rows 4 (a) and 8 (x) banks apart
+    static constexpr int kXPitch = kWide ? kPos + 8 : kPos + 8;
+    static constexpr int kAPitch = kWide ? kChan + 4 : kChan + 8;
+    static constexpr int kXBytes = kChan * kXPitch * (int)sizeof(T);
+    static constexpr int kStage = kXBytes + RP * kAPitch * (int)sizeof(T);
+    static constexpr int kVPitch = kPos + 4;
+    static constexpr int kV = RP * kVPitch * 4;
+    static constexpr int kSmem = kStages * kStage + 2 * kV;
+};
+
+// One stage: channels c0 .. c0 + 63 of the tile's positions and of a's rows.
+template <typename T, int RT>
+static __device__ __forceinline__ void fetch_stage(const AdapterParams &p, unsigned char *stage,
+                                                   const T *x, const T *a, int c0, int p0) {
+    using G = PromptTile<T, RT>;
+    constexpr int V = G::kVec;
+    T *xs = reinterpret_cast<T *>(stage), *as = reinterpret_cast<T *>(stage + G::kXBytes);
+    if (p.vec_x) {
+        for (int i = threadIdx.x; i < kChan * (kPos / V); i += kThreads) {
+            const int c = i / (kPos / V), q = i % (kPos / V) * V;
+            const bool on = c0 + c < p.C && p0 + q < p.P;  // rows are whole vectors
+            copy16(xs + c * G::kXPitch + q, on ? x + (int64_t)(c0 + c) * p.x_sc + p0 + q : x, on);
+        }
+    } else {
+        for (int i = threadIdx.x; i < kChan * kPos; i += kThreads) {
+            const int c = i / kPos, q = i % kPos;
+            xs[c * G::kXPitch + q] = c0 + c < p.C && p0 + q < p.P
+                                         ? x[(int64_t)(c0 + c) * p.x_sc + p0 + q]
+                                         : from_f32<T>(0.f);
+        }
+    }
+    if (p.vec_a) {
+        for (int i = threadIdx.x; i < G::RP * (kChan / V); i += kThreads) {
+            const int r = i / (kChan / V), q = i % (kChan / V) * V;
+            const bool on = r < p.R && c0 + q < p.C;
+            copy16(as + r * G::kAPitch + q, on ? a + (int64_t)r * p.C + c0 + q : a, on);
+        }
+    } else {
+        for (int i = threadIdx.x; i < G::RP * kChan; i += kThreads) {
+            const int r = i / kChan, q = i % kChan;
+            as[r * G::kAPitch + q] =
+                r < p.R && c0 + q < p.C ? a[(int64_t)r * p.C + c0 + q] : from_f32<T>(0.f);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Runs of eight positions (16-bit) or four (32-bit) of y, eight positions in
+// all, zeros where there are none.
+template <typename T>
+struct Eight {
+    static constexpr int V = 16 / sizeof(T), K = 8 / V;
+    Run<T, V> r[K];
+    __device__ __forceinline__ void load(const T *row, int at, int end, bool vec) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) load_run(r[k], row, at + k * V, end, vec);
+    }
+    __device__ __forceinline__ float get(int i) const { return r[i / V][i % V]; }
+    __device__ __forceinline__ void store(const float (&v)[8], T *row, int at, int end, bool vec) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float w[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] = v[k * V + i];
+            r[k].put(w);
+            store_run(r[k], row, at + k * V, end, vec);
+        }
+    }
+};
+
+template <typename T, int RT>
+__global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p) {
+    using G = PromptTile<T, RT>;
+    constexpr bool kWide = G::kWide;
+    extern __shared__ __align__(128) unsigned char smem[];
+    float *part = reinterpret_cast<float *>(smem + kStages * G::kStage);  // [RP][kVPitch]
+    float *v = part + G::kV / 4;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const int job = blockIdx.x / ranks;
+    const int n = job / p.tiles, p0 = (job - n * p.tiles) * kPos;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, j = lane & 3;
+    const int id = adapter_of(p, n);
+    const T *y = static_cast<const T *>(p.y) + (int64_t)n * p.M * p.P;
+    T *out = static_cast<T *>(p.out) + (int64_t)n * p.M * p.P;
+
+    // rows of the output that are this block's; a warp takes 16 at a time of one
+    // half of the positions, eight consecutive ones of two rows in each lane
+    const int mtiles = (p.M + 15) / 16;
+    const int m_first = (int)((int64_t)mtiles * rank / ranks);
+    const int m_last = (int)((int64_t)mtiles * (rank + 1) / ranks);
+    const int half = p0 + (warp >> 1) * 32, at = half + j * 8;
+    if (id < 0) {  // the same for the whole cluster
+        if (static_cast<const void *>(out) == y) return;
+        for (int m = m_first + (warp & 1); m < m_last; m += 2)
+            for (int k = 0; k < 2; ++k) {
+                const int row = m * 16 + g + 8 * k;
+                if (row >= p.M) continue;
+                Eight<T> e;
+                e.load(y + (int64_t)row * p.P, at, p.P, p.vec_y);
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = e.get(i);
+                e.store(f, out + (int64_t)row * p.P, at, p.P, p.vec_y);
+            }
+        return;
+    }
+    const T *x = static_cast<const T *>(p.x) + n * p.x_sn;
+    const T *a = static_cast<const T *>(p.a) + (int64_t)id * p.R * p.C;
+    const T *b = static_cast<const T *>(p.b) + (int64_t)id * p.M * p.R;
+    const float scale = p.scale ? p.scale[id] : 1.f;
+
+    // v = a x over this block's channels; a warp has 16 of the positions
+    {
+        const int stages = (p.C + kChan - 1) / kChan;
+        const int first = (int)((int64_t)stages * rank / ranks);
+        const int last = (int)((int64_t)stages * (rank + 1) / ranks);
+        float acc[RT][2][4];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[r][q][i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) {
+            if (first + k < last)
+                fetch_stage<T, RT>(p, smem + k * G::kStage, x, a, (first + k) * kChan, p0);
+            else
+                asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        for (int s = first; s < last; ++s) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncthreads();  // the stage has arrived, and the one to be fetched is free
+            const int ahead = s + kStages - 1;
+            if (ahead < last)
+                fetch_stage<T, RT>(p, smem + (ahead - first) % kStages * G::kStage, x, a,
+                                   ahead * kChan, p0);
+            else
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            const unsigned char *stage = smem + (s - first) % kStages * G::kStage;
+            const T *xs = reinterpret_cast<const T *>(stage);
+            const T *as = reinterpret_cast<const T *>(stage + G::kXBytes);
+            if constexpr (!kWide) {
+#pragma unroll
+                for (int k = 0; k < kChan; k += 16) {
+                    uint32_t xb[4];
+                    ldmatrix4_trans(xb, xs + (k + (lane & 15)) * G::kXPitch + warp * 16 + (lane >> 4) * 8);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        uint32_t aa[4];
+                        ldmatrix4(aa, as + (r * 16 + (lane & 15)) * G::kAPitch + k + (lane >> 4) * 8);
+                        mma16<T>(acc[r][0], aa, xb[0], xb[1]);
+                        mma16<T>(acc[r][1], aa, xb[2], xb[3]);
+                    }
+                }
+            } else {
+#pragma unroll 4
+                for (int k = 0; k < kChan; k += 8) {
+                    uint32_t xh[2][2], xl[2][2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            split_tf32(to_f32(xs[(k + j + 4 * i) * G::kXPitch + warp * 16 + q * 8 + g]),
+                                       xh[q][i], xl[q][i]);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        uint32_t ah[4], al[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            split_tf32(to_f32(as[(r * 16 + g + 8 * (i & 1)) * G::kAPitch + k + j +
+                                                 4 * (i >> 1)]),
+                                       ah[i], al[i]);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            mma8(acc[r][q], al, xh[q][0], xh[q][1]);
+                            mma8(acc[r][q], ah, xl[q][0], xl[q][1]);
+                            mma8(acc[r][q], ah, xh[q][0], xh[q][1]);
+                        }
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        // rows behind R are zero whatever x holds
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = r * 16 + g + 8 * (i >> 1);
+                    part[row * G::kVPitch + warp * 16 + q * 8 + 2 * j + (i & 1)] =
+                        row < p.R ? acc[r][q][i] : 0.f;
+                }
+    }
+    if (ranks > 1) {
+        cluster.sync();
+        // each block adds a share of v over the ranks and hands it to all
+        for (int i = rank * kThreads + threadIdx.x; i < G::RP * kPos / 4; i += ranks * kThreads) {
+            const int o = i / (kPos / 4) * G::kVPitch + i % (kPos / 4) * 4;
+            float4 t = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(part, 0) + o);
+            for (int k = 1; k < ranks; ++k) {
+                const float4 f = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(part, k) + o);
+                t.x += f.x; t.y += f.y; t.z += f.z; t.w += f.w;
+            }
+            for (int k = 0; k < ranks; ++k)
+                *reinterpret_cast<float4 *>(cluster.map_shared_rank(v, k) + o) = t;
+        }
+        cluster.sync();
+    } else {
+        v = part;
+        __syncthreads();
+    }
+
+    // out = y + scale b v.  Column q of the four tiles of eight that a warp
+    // multiplies stands for position 8 (q / 2) + 2 tile + q % 2 of its half, so
+    // that a lane's results are eight consecutive positions.
+    constexpr int KS = RT * 2;  // steps of eight rows of v
+    uint32_t vh[KS][4][2], vl[KS][4][2];  // (16-bit: the words of steps 2k, 2k + 1 are one step of 16)
+    constexpr bool kPairs = std::is_same<T, __nv_bfloat16>::value;
+#pragma unroll
+    for (int k = 0; k < (kPairs ? RT : KS); ++k)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float *col = v + (warp >> 1) * 32 + (g >> 1) * 8 + 2 * t + (g & 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (kPairs) {
+                    const float *at2 = col + (k * 16 + i * 8 + 2 * j) * G::kVPitch;
+                    split_bf16(at2[0], at2[G::kVPitch], vh[k][t][i], vl[k][t][i]);
+                } else {
+                    split_tf32(col[(k * 8 + i * 4 + j) * G::kVPitch], vh[k][t][i], vl[k][t][i]);
+                }
+            }
+        }
+    for (int m = m_first + (warp & 1); m < m_last; m += 2) {
+        const int r0 = m * 16 + g, r1 = r0 + 8;
+        Eight<T> e0, e1;
+        e0.load(y + (int64_t)r0 * p.P, at, r0 < p.M ? p.P : 0, p.vec_y);
+        e1.load(y + (int64_t)r1 * p.P, at, r1 < p.M ? p.P : 0, p.vec_y);
+        float acc[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+        if constexpr (kPairs) {
+#pragma unroll
+            for (int k = 0; k < RT; ++k) {
+                uint32_t bb[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = i & 1 ? r1 : r0, c = k * 16 + (i >> 1) * 8 + 2 * j;
+                    const T *q = b + (int64_t)row * p.R + c;
+                    bb[i] = 0;
+                    if (row < p.M) {
+                        if (p.vec_b && c + 1 < p.R)
+                            bb[i] = *reinterpret_cast<const uint32_t *>(q);
+                        else
+                            bb[i] = (c < p.R ? bits_of(q[0]) : 0u) |
+                                    (c + 1 < p.R ? bits_of(q[1]) << 16 : 0u);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    mma16<T>(acc[t], bb, vl[k][t][0], vl[k][t][1]);
+                    mma16<T>(acc[t], bb, vh[k][t][0], vh[k][t][1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t bh[4], bl[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = i & 1 ? r1 : r0, c = k * 8 + (i >> 1) * 4 + j;
+                    const float f = row < p.M && c < p.R ? to_f32(b[(int64_t)row * p.R + c]) : 0.f;
+                    split_tf32(f, bh[i], bl[i]);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if constexpr (kWide) mma8(acc[t], bl, vh[k][t][0], vh[k][t][1]);
+                    mma8(acc[t], bh, vl[k][t][0], vl[k][t][1]);
+                    mma8(acc[t], bh, vh[k][t][0], vh[k][t][1]);
+                }
+            }
+        }
+        float f0[8], f1[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f0[2 * t + i] = fmaf(scale, acc[t][i], e0.get(2 * t + i));
+                f1[2 * t + i] = fmaf(scale, acc[t][2 + i], e1.get(2 * t + i));
+            }
+        if (r0 < p.M) e0.store(f0, out + (int64_t)r0 * p.P, at, p.P, p.vec_y);
+        if (r1 < p.M) e1.store(f1, out + (int64_t)r1 * p.P, at, p.P, p.vec_y);
+    }
+}
+
+// ---------------------------------------------------------------- single tokens
+
+constexpr int kTokenThreads = 256, kTokenWarps = kTokenThreads / 32;
+constexpr int kMaxRanks = 8;
+constexpr int kMaxR = 64;
+
+// A cluster per token.  A warp sums two rows of a at a time over the block's
+// channels, every block adds the ranks' parts of v, a thread sums rows of b.
+// What does not depend on v -- the first rows of b, of y -- is read before it.
+template <typename T>
+__global__ void __launch_bounds__(kTokenThreads) token_kernel(const AdapterParams p) {
+    __shared__ float part[kMaxR];
+    __shared__ __align__(16) float v[kMaxR];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
+    const int n = blockIdx.x / ranks;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int id = adapter_of(p, n);
+    const T *y = static_cast<const T *>(p.y) + (int64_t)n * p.M;
+    T *out = static_cast<T *>(p.out) + (int64_t)n * p.M;
+    const int m_first = (int)((int64_t)p.M * rank / ranks);
+    const int m_last = (int)((int64_t)p.M * (rank + 1) / ranks);
+    if (id < 0) {  // the same for the whole cluster
+        for (int m = m_first + threadIdx.x; m < m_last; m += kTokenThreads) out[m] = y[m];
+        return;
+    }
+    const T *x = static_cast<const T *>(p.x) + n * p.x_sn;
+    const T *a = static_cast<const T *>(p.a) + (int64_t)id * p.R * p.C;
+    const T *b = static_cast<const T *>(p.b) + (int64_t)id * p.M * p.R;
+    const float scale = p.scale ? p.scale[id] : 1.f;
+    constexpr int V = 16 / sizeof(T), kEarly = 2;
+    // channels in whole vectors, so that a block's slice starts on one
+    const int vectors = (p.C + V - 1) / V;
+    const int c_first = (int)((int64_t)vectors * rank / ranks) * V;
+    const int c_last = min(p.C, (int)((int64_t)vectors * (rank + 1) / ranks) * V);
+    const int m0 = m_first + threadIdx.x;
+    Run<T, V> early[kEarly];
+    float y0 = 0.f;
+#pragma unroll
+    for (int k = 0; k < kEarly; ++k)
+        load_run(early[k], b + (int64_t)m0 * p.R, k * V, m0 < m_last ? p.R : 0, p.vec_b);
+    if (m0 < m_last) y0 = to_f32(y[m0]);
+    for (int r0 = warp * 2; r0 < p.R; r0 += kTokenWarps * 2) {
+        float s[2] = {0.f, 0.f};
+        const bool two = r0 + 1 < p.R;
+        const T *row = a + (int64_t)r0 * p.C;
+#pragma unroll 2
+        for (int c = c_first + lane * V; c < c_last; c += 32 * V) {
+            Run<T, V> xr, ar, br;
+            if (p.x_sc == 1) {
+                load_run(xr, x, c, c_last, p.vec_x);
+            } else {
+                float f[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[i] = c + i < c_last ? to_f32(x[(c + i) * p.x_sc]) : 0.f;
+                xr.put(f);
+            }
+            load_run(ar, row, c, c_last, p.vec_a);
+            load_run(br, row + p.C, c, two ? c_last : 0, p.vec_a);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                s[0] = fmaf(ar[i], xr[i], s[0]);
+                s[1] = fmaf(br[i], xr[i], s[1]);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            s[0] += __shfl_xor_sync(~0u, s[0], o);
+            s[1] += __shfl_xor_sync(~0u, s[1], o);
+        }
+        if (lane == 0) {
+            part[r0] = s[0];
+            if (two) part[r0 + 1] = s[1];
+        }
+    }
+    cluster.sync();
+    if (threadIdx.x < kMaxR) {
+        float t = 0.f;
+        if (threadIdx.x < p.R)
+            for (int k = 0; k < ranks; ++k) t += cluster.map_shared_rank(part, k)[threadIdx.x];
+        v[threadIdx.x] = t;
+    }
+    __syncthreads();
+    auto left = cluster.barrier_arrive();  // this block has read the others' parts
+    for (int m = m0; m < m_last; m += kTokenThreads) {
+        const T *row = b + (int64_t)m * p.R;
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxR / V; ++k) {
+            if (k * V >= p.R) break;
+            Run<T, V> br;
+            if (k < kEarly && m == m0)
+                br = early[k < kEarly ? k : 0];
+            else
+                load_run(br, row, k * V, p.R, p.vec_b);
+            // (behind R both are zero)
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(v + k * V + i);
+                s = fmaf(br[i], f.x, s);
+                s = fmaf(br[i + 1], f.y, s);
+                s = fmaf(br[i + 2], f.z, s);
+                s = fmaf(br[i + 3], f.w, s);
+            }
+        }
+        out[m] = from_f32<T>(fmaf(scale, s, m == m0 ? y0 : to_f32(y[m])));
+    }
+    cluster.barrier_wait(std::move(left));  // its own part may go once all have
+}
+
+// ---------------------------------------------------------------- host side
 
 int check_sizes(const spconv_adapter_args *a) {
     if (!a || a->N < 0 || a->P < 0 || a->C < 0 || a->M < 0 || a->R < 1 || a->adapters < 0)
         return SPCONV_ERR_INVALID_ARG;
     if (a->dtype < SPCONV_F32 || a->dtype > SPCONV_F16) return SPCONV_ERR_INVALID_ARG;
     if (!stride_ok(a->x_stride_n) || !stride_ok(a->x_stride_c)) return SPCONV_ERR_INVALID_ARG;
-    return a->R > 64 ? SPCONV_ERR_UNSUPPORTED : SPCONV_OK;
+    return a->R > kMaxR ? SPCONV_ERR_UNSUPPORTED : SPCONV_OK;
+}
+
+// Launches `jobs` clusters of `ranks` blocks.
+int launch_clusters(void (*fn)(AdapterParams), int64_t jobs, int ranks, int threads, int smem,
+                    const AdapterParams &p, cudaStream_t stream) {
+    if (jobs * ranks > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
+    if (smem > 48 * 1024 &&
+        cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+        cudaGetLastError();
+        return SPCONV_ERR_CUDA;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(jobs * ranks));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
+        cudaGetLastError();
+        return SPCONV_ERR_CUDA;
+    }
+    return SPCONV_OK;
+}
+
+// Blocks of a cluster: twice as many until there are `want` blocks, as long as
+// each has `least` of both the channels and the rows.
+int ranks_for(const AdapterParams &p, int64_t jobs, int64_t want, int least) {
+    int r = 1;
+    const int small = p.C < p.M ? p.C : p.M;
+    while (r < kMaxRanks && jobs * r < want && small / (2 * r) >= least) r *= 2;
+    return r;
 }
 
 }  // namespace
@@ -75,8 +580,8 @@ int check_sizes(const spconv_adapter_args *a) {
 using namespace spconv::seq;
 
 SPCONV_API int64_t spconv_adapter_workspace(const spconv_adapter_args *a) {
-    if (check_sizes(a)) return 0;
-    return (int64_t)a->N * a->R * a->P * 4;
+    (void)a;
+    return 0;
 }
 
 SPCONV_API int spconv_adapter_add(const spconv_adapter_args *a, void *stream) {
@@ -91,9 +596,6 @@ SPCONV_API int spconv_adapter_add(const spconv_adapter_args *a, void *stream) {
     for (const void *q : {a->x, a->a, a->b, a->y, (const void *)a->out})
         if (!aligned(q, e)) return SPCONV_ERR_INVALID_ARG;
     if (!aligned(a->index, 4) || !aligned(a->scale, 4)) return SPCONV_ERR_INVALID_ARG;
-    const int64_t need = spconv_adapter_workspace(a);
-    if (need && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need))
-        return SPCONV_ERR_INVALID_ARG;
     const int64_t ab = (int64_t)a->adapters * a->R * e;
     if ((a->out != a->y && overlap(a->out, out * e, a->y, out * e)) ||
         overlap(a->out, out * e, a->x, extent(a->N, a->C, a->P, a->x_stride_n, a->x_stride_c, e)) ||
@@ -101,17 +603,34 @@ SPCONV_API int spconv_adapter_add(const spconv_adapter_args *a, void *stream) {
         return SPCONV_ERR_INVALID_ARG;
     AdapterParams p{};
     p.x = a->x; p.a = a->a; p.b = a->b; p.y = a->y; p.index = a->index; p.scale = a->scale;
-    p.out = a->out; p.v = static_cast<float *>(a->workspace);
+    p.out = a->out;
     p.x_sn = a->x_stride_n; p.x_sc = a->x_stride_c;
     p.N = a->N; p.P = a->P; p.C = a->C; p.M = a->M; p.R = a->R; p.adapters = a->adapters;
-    const int64_t inner = (int64_t)a->N * a->R * a->P;
-    const int64_t bi = (inner + kThreads - 1) / kThreads, bo = (out + kThreads - 1) / kThreads;
-    if (bi > 0x7fffffff || bo > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
+    p.vec_a = rows_aligned(a->a, 0, a->C, e);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a->P == 1) {
+        p.vec_x = rows_aligned(a->x, a->x_stride_n, 0, e);
+        p.vec_b = rows_aligned(a->b, 0, a->R, e);
+        return by_dtype(a->dtype, [&](auto t) {
+            return launch_clusters(token_kernel<decltype(t)>, p.N, ranks_for(p, p.N, 4 * kSMs, 64),
+                                   kTokenThreads, 0, p, s);
+        });
+    }
+    p.tiles = (int)(((int64_t)a->P + kPos - 1) / kPos);
+    p.vec_x = rows_aligned(a->x, a->x_stride_n, a->x_stride_c, e) && a->P * e % 16 == 0;
+    p.vec_y = rows_aligned(a->y, 0, a->P, e) && rows_aligned(a->out, 0, a->P, e);
+    p.vec_b = aligned(a->b, 4) && a->R % 2 == 0;
+    const int64_t jobs = (int64_t)p.N * p.tiles;
+    const int ranks = ranks_for(p, jobs, 4 * kSMs, 64);
     return by_dtype(a->dtype, [&](auto t) {
         using T = decltype(t);
-        shrink_kernel<T><<<(unsigned)bi, kThreads, 0, s>>>(p);
-        expand_kernel<T><<<(unsigned)bo, kThreads, 0, s>>>(p);
-        return launch_status();
+        auto go = [&](auto rt) {
+            constexpr int RT = decltype(rt)::value;
+            return launch_clusters(prompt_kernel<T, RT>, jobs, ranks, kThreads,
+                                   PromptTile<T, RT>::kSmem, p, s);
+        };
+        if (a->R <= 16) return go(std::integral_constant<int, 1>{});
+        if (a->R <= 32) return go(std::integral_constant<int, 2>{});
+        return go(std::integral_constant<int, 4>{});
     });
 }

@@ -32,9 +32,9 @@ struct ScanTile {
     static constexpr int NI = CW * 4 / 32;                  // loads of a lane from each row set
     static constexpr int NB = 2 * SP * 4 / 32;              // from B and C
     // in rows of 16 bytes {dt, dt u} of a pair's channels: one more after every
-    // VE positions, and odd, so that neither the lanes that write nor the pairs
-    // that read meet in few banks
-    static constexpr int kStepPitch = TT + 7;
+    // VE positions, and 2 modulo 8, so that neither the lanes that write nor the
+    // pairs that read meet in the same banks
+    static constexpr int kStepPitch = TT + 10;
     static constexpr int kOutPitch = TT + 4;
     static constexpr int kOutHalf = PAIRS * kOutPitch + 16;  // from the pairs' first channels to
                                                              // their second
