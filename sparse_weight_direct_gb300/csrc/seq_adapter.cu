@@ -75,11 +75,12 @@ static __device__ __forceinline__ void split_tf32(float v, uint32_t &hi, uint32_
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(fabsf(v) <= 3.402e38f ? rest : 0.f));
 }
 // two values as words of 16-bit parts: hi, and what hi leaves
-static __device__ __forceinline__ void split_bf16(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = f32_to_word<__nv_bfloat16>(a, b);
-    const float2 h = word_to_f32<__nv_bfloat16>(hi);
-    lo = f32_to_word<__nv_bfloat16>(fabsf(a) <= 3.38e38f ? a - h.x : 0.f,
-                                    fabsf(b) <= 3.38e38f ? b - h.y : 0.f);
+template <typename T>
+static __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = f32_to_word<T>(a, b);
+    const float2 h = word_to_f32<T>(hi);
+    lo = f32_to_word<T>(fabsf(h.x) <= 3.4e38f ? a - h.x : 0.f,
+                        fabsf(h.y) <= 3.4e38f ? b - h.y : 0.f);
 }
 
 static __device__ __forceinline__ uint32_t smem_address(const void *p) {
@@ -105,7 +106,6 @@ static __device__ __forceinline__ void copy16(void *to, const void *from, bool o
 // ---------------------------------------------------------------- prompts
 
 constexpr int kPos = 64;    // positions of a tile
-constexpr int kChan = 64;   // channels of a stage
 constexpr int kStages = 3;
 constexpr int kThreads = 128;
 
@@ -113,6 +113,7 @@ template <typename T, int RT>
 struct PromptTile {
     static constexpr bool kWide = sizeof(T) == 4;
     static constexpr int RP = 16 * RT;  // rows of a, padded
+    static constexpr int kChan = kWide ? 32 : 64;  // channels of a stage
     static constexpr int kVec = 16 / sizeof(T);
     // pitches in elements: the eight rows of a matrix read start in different
     // banks; 32-bit fragments take rows 4 (a) and 8 (x) banks apart
@@ -122,15 +123,17 @@ struct PromptTile {
     static constexpr int kStage = kXBytes + RP * kAPitch * (int)sizeof(T);
     static constexpr int kVPitch = kPos + 4;
     static constexpr int kV = RP * kVPitch * 4;
-    static constexpr int kSmem = kStages * kStage + 2 * kV;
+    // the block's part of v takes the place of the stages
+    static constexpr int kFront = kStages * kStage > kV ? kStages * kStage : kV;
+    static constexpr int kSmem = kFront + kV;
 };
 
-// One stage: channels c0 .. c0 + 63 of the tile's positions and of a's rows.
+// One stage: kChan channels from c0 of the tile's positions and of a's rows.
 template <typename T, int RT>
 static __device__ __forceinline__ void fetch_stage(const AdapterParams &p, unsigned char *stage,
                                                    const T *x, const T *a, int c0, int p0) {
     using G = PromptTile<T, RT>;
-    constexpr int V = G::kVec;
+    constexpr int V = G::kVec, kChan = G::kChan;
     T *xs = reinterpret_cast<T *>(stage), *as = reinterpret_cast<T *>(stage + G::kXBytes);
     if (p.vec_x) {
         for (int i = threadIdx.x; i < kChan * (kPos / V); i += kThreads) {
@@ -189,9 +192,10 @@ template <typename T, int RT>
 __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p) {
     using G = PromptTile<T, RT>;
     constexpr bool kWide = G::kWide;
+    constexpr int kChan = G::kChan;
     extern __shared__ __align__(128) unsigned char smem[];
-    float *part = reinterpret_cast<float *>(smem + kStages * G::kStage);  // [RP][kVPitch]
-    float *v = part + G::kV / 4;
+    float *part = reinterpret_cast<float *>(smem);              // [RP][kVPitch]
+    float *v = reinterpret_cast<float *>(smem + G::kFront);     // likewise
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const int job = blockIdx.x / ranks;
@@ -226,6 +230,47 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
     const T *a = static_cast<const T *>(p.a) + (int64_t)id * p.R * p.C;
     const T *b = static_cast<const T *>(p.b) + (int64_t)id * p.M * p.R;
     const float scale = p.scale ? p.scale[id] : 1.f;
+
+    // the rows of y and b that a warp takes next are on their way while it
+    // multiplies, the first ones while v is formed
+    constexpr bool kPairs = !kWide;  // products of 16-bit parts
+    constexpr bool kAhead = kPairs || RT <= 2;  // (32-bit rows of more would not fit)
+    struct Next {
+        Eight<T> e0, e1;
+        uint32_t b[kPairs ? RT : kAhead ? 2 * RT : 1][4];
+    } next;
+    auto fetch_rows = [&](int m) {
+        const int r0 = m * 16 + g, r1 = r0 + 8;
+        const bool on = m < m_last;
+        next.e0.load(y + (int64_t)r0 * p.P, at, on && r0 < p.M ? p.P : 0, p.vec_y);
+        next.e1.load(y + (int64_t)r1 * p.P, at, on && r1 < p.M ? p.P : 0, p.vec_y);
+        if constexpr (kPairs) {
+#pragma unroll
+            for (int k = 0; k < RT; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = i & 1 ? r1 : r0, c = k * 16 + (i >> 1) * 8 + 2 * j;
+                    const T *q = b + (int64_t)row * p.R + c;
+                    next.b[k][i] = 0;
+                    if (on && row < p.M) {
+                        if (p.vec_b && c + 1 < p.R)
+                            next.b[k][i] = *reinterpret_cast<const uint32_t *>(q);
+                        else
+                            next.b[k][i] = (c < p.R ? bits_of(q[0]) : 0u) |
+                                           (c + 1 < p.R ? bits_of(q[1]) << 16 : 0u);
+                    }
+                }
+        } else if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < 2 * RT; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = i & 1 ? r1 : r0, c = k * 8 + (i >> 1) * 4 + j;
+                    next.b[k][i] = on && row < p.M && c < p.R ? bits_of(b[(int64_t)row * p.R + c]) : 0;
+                }
+        }
+    };
+    fetch_rows(m_first + (warp & 1));
 
     // v = a x over this block's channels; a warp has 16 of the positions
     {
@@ -300,6 +345,7 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
         // rows behind R are zero whatever x holds
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -334,19 +380,36 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
     // out = y + scale b v.  Column q of the four tiles of eight that a warp
     // multiplies stands for position 8 (q / 2) + 2 tile + q % 2 of its half, so
     // that a lane's results are eight consecutive positions.
+    constexpr bool kHalf = std::is_same<T, __half>::value;
     constexpr int KS = RT * 2;  // steps of eight rows of v
+    __shared__ float units[kHalf ? kPos : 1];
+    float unit[8];  // of the lane's positions
+    if constexpr (kHalf) {
+        // 16-bit floats do not reach as far as sums of their products: each position's
+        // v is scaled to at most 2 by a power of two, and its products back
+        if (threadIdx.x < kPos) {
+            float most = 0.f;
+            for (int r = 0; r < p.R; ++r) most = fmaxf(most, fabsf(v[r * G::kVPitch + threadIdx.x]));
+            const uint32_t e = __float_as_uint(most) & 0x7f800000u;
+            units[threadIdx.x] = e == 0 || e >= 0x7f000000u ? 1.f : __uint_as_float(e);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) unit[i] = units[(warp >> 1) * 32 + j * 8 + i];
+    }
     uint32_t vh[KS][4][2], vl[KS][4][2];  // (16-bit: the words of steps 2k, 2k + 1 are one step of 16)
-    constexpr bool kPairs = std::is_same<T, __nv_bfloat16>::value;
 #pragma unroll
     for (int k = 0; k < (kPairs ? RT : KS); ++k)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const float *col = v + (warp >> 1) * 32 + (g >> 1) * 8 + 2 * t + (g & 1);
+            const int pos = (warp >> 1) * 32 + (g >> 1) * 8 + 2 * t + (g & 1);
+            const float *col = v + pos;
+            const float down = kHalf ? 1.f / units[kHalf ? pos : 0] : 1.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if constexpr (kPairs) {
                     const float *at2 = col + (k * 16 + i * 8 + 2 * j) * G::kVPitch;
-                    split_bf16(at2[0], at2[G::kVPitch], vh[k][t][i], vl[k][t][i]);
+                    split_pair<T>(at2[0] * down, at2[G::kVPitch] * down, vh[k][t][i], vl[k][t][i]);
                 } else {
                     split_tf32(col[(k * 8 + i * 4 + j) * G::kVPitch], vh[k][t][i], vl[k][t][i]);
                 }
@@ -354,9 +417,8 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         }
     for (int m = m_first + (warp & 1); m < m_last; m += 2) {
         const int r0 = m * 16 + g, r1 = r0 + 8;
-        Eight<T> e0, e1;
-        e0.load(y + (int64_t)r0 * p.P, at, r0 < p.M ? p.P : 0, p.vec_y);
-        e1.load(y + (int64_t)r1 * p.P, at, r1 < p.M ? p.P : 0, p.vec_y);
+        Next now = next;
+        fetch_rows(m + 2);
         float acc[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -365,24 +427,10 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         if constexpr (kPairs) {
 #pragma unroll
             for (int k = 0; k < RT; ++k) {
-                uint32_t bb[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = i & 1 ? r1 : r0, c = k * 16 + (i >> 1) * 8 + 2 * j;
-                    const T *q = b + (int64_t)row * p.R + c;
-                    bb[i] = 0;
-                    if (row < p.M) {
-                        if (p.vec_b && c + 1 < p.R)
-                            bb[i] = *reinterpret_cast<const uint32_t *>(q);
-                        else
-                            bb[i] = (c < p.R ? bits_of(q[0]) : 0u) |
-                                    (c + 1 < p.R ? bits_of(q[1]) << 16 : 0u);
-                    }
-                }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    mma16<T>(acc[t], bb, vl[k][t][0], vl[k][t][1]);
-                    mma16<T>(acc[t], bb, vh[k][t][0], vh[k][t][1]);
+                    mma16<T>(acc[t], now.b[k], vl[k][t][0], vl[k][t][1]);
+                    mma16<T>(acc[t], now.b[k], vh[k][t][0], vh[k][t][1]);
                 }
             }
         } else {
@@ -392,12 +440,13 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = i & 1 ? r1 : r0, c = k * 8 + (i >> 1) * 4 + j;
-                    const float f = row < p.M && c < p.R ? to_f32(b[(int64_t)row * p.R + c]) : 0.f;
+                    const float f = kAhead ? __uint_as_float(now.b[kAhead ? k : 0][i])
+                                    : row < p.M && c < p.R ? to_f32(b[(int64_t)row * p.R + c]) : 0.f;
                     split_tf32(f, bh[i], bl[i]);
                 }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    if constexpr (kWide) mma8(acc[t], bl, vh[k][t][0], vh[k][t][1]);
+                    mma8(acc[t], bl, vh[k][t][0], vh[k][t][1]);
                     mma8(acc[t], bh, vl[k][t][0], vl[k][t][1]);
                     mma8(acc[t], bh, vh[k][t][0], vh[k][t][1]);
                 }
@@ -408,11 +457,12 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                f0[2 * t + i] = fmaf(scale, acc[t][i], e0.get(2 * t + i));
-                f1[2 * t + i] = fmaf(scale, acc[t][2 + i], e1.get(2 * t + i));
+                const float up = kHalf ? scale * unit[2 * t + i] : scale;
+                f0[2 * t + i] = fmaf(up, acc[t][i], now.e0.get(2 * t + i));
+                f1[2 * t + i] = fmaf(up, acc[t][2 + i], now.e1.get(2 * t + i));
             }
-        if (r0 < p.M) e0.store(f0, out + (int64_t)r0 * p.P, at, p.P, p.vec_y);
-        if (r1 < p.M) e1.store(f1, out + (int64_t)r1 * p.P, at, p.P, p.vec_y);
+        if (r0 < p.M) now.e0.store(f0, out + (int64_t)r0 * p.P, at, p.P, p.vec_y);
+        if (r1 < p.M) now.e1.store(f1, out + (int64_t)r1 * p.P, at, p.P, p.vec_y);
     }
 }
 
