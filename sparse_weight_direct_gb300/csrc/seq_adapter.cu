@@ -123,8 +123,12 @@ struct PromptTile {
     static constexpr int kStage = kXBytes + RP * kAPitch * (int)sizeof(T);
     static constexpr int kVPitch = kPos + 4;
     static constexpr int kV = RP * kVPitch * 4;
-    // the block's part of v takes the place of the stages
-    static constexpr int kFront = kStages * kStage > kV ? kStages * kStage : kV;
+    // Behind the products the stages' place is taken by the block's part of v
+    // and by rows of y on their way: tiles of 16 x 32 for each warp.
+    static constexpr int kDepth = kWide ? 4 : 6;
+    static constexpr int kRing = kDepth * (kThreads / 32) * 16 * 32 * (int)sizeof(T);
+    static constexpr int kFront =
+        kStages * kStage > kV + kRing ? kStages * kStage : kV + kRing;
     static constexpr int kSmem = kFront + kV;
 };
 
@@ -174,6 +178,10 @@ struct Eight {
     __device__ __forceinline__ void load(const T *row, int at, int end, bool vec) {
 #pragma unroll
         for (int k = 0; k < K; ++k) load_run(r[k], row, at + k * V, end, vec);
+    }
+    __device__ __forceinline__ void read(const T *shared) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) r[k] = reinterpret_cast<const Run<T, V> *>(shared)[k];
     }
     __device__ __forceinline__ float get(int i) const { return r[i / V][i % V]; }
     __device__ __forceinline__ void store(const float (&v)[8], T *row, int at, int end, bool vec) {
@@ -231,33 +239,38 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
     const T *b = static_cast<const T *>(p.b) + (int64_t)id * p.M * p.R;
     const float scale = p.scale ? p.scale[id] : 1.f;
 
-    // the rows of y and b that a warp takes next are on their way while it
-    // multiplies, the first ones while v is formed
+    // what a warp takes next of b is on its way while it multiplies
     constexpr bool kPairs = !kWide;  // products of 16-bit parts
     constexpr bool kAhead = kPairs || RT <= 2;  // (32-bit rows of more would not fit)
-    struct Next {
-        Eight<T> e0, e1;
-        uint32_t b[kPairs ? RT : kAhead ? 2 * RT : 1][4];
-    } next;
-    auto fetch_rows = [&](int m) {
+    uint32_t next[kPairs ? RT : kAhead ? 2 * RT : 1][4];
+    const int m_own = m_first + (warp & 1);
+    const bool whole_b = p.vec_b && p.R == G::RP;
+    auto fetch_b = [&](int m) {
         const int r0 = m * 16 + g, r1 = r0 + 8;
-        const bool on = m < m_last;
-        next.e0.load(y + (int64_t)r0 * p.P, at, on && r0 < p.M ? p.P : 0, p.vec_y);
-        next.e1.load(y + (int64_t)r1 * p.P, at, on && r1 < p.M ? p.P : 0, p.vec_y);
-        if constexpr (kPairs) {
+        if (kAhead && whole_b && m < m_last && m * 16 + 16 <= p.M) {
+            // whole rows of words
+            constexpr int kRow = kPairs ? RT * 8 : RT * 16;
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(b) + (int64_t)r0 * kRow + j;
+#pragma unroll
+            for (int k = 0; k < (kPairs ? RT : 2 * RT); ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    next[kAhead ? k : 0][i] =
+                        __ldg(q + (i & 1) * (8 * kRow) + k * 8 + (i >> 1) * 4);
+        } else if constexpr (kPairs) {
 #pragma unroll
             for (int k = 0; k < RT; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = i & 1 ? r1 : r0, c = k * 16 + (i >> 1) * 8 + 2 * j;
                     const T *q = b + (int64_t)row * p.R + c;
-                    next.b[k][i] = 0;
-                    if (on && row < p.M) {
+                    next[k][i] = 0;
+                    if (m < m_last && row < p.M) {
                         if (p.vec_b && c + 1 < p.R)
-                            next.b[k][i] = *reinterpret_cast<const uint32_t *>(q);
+                            next[k][i] = *reinterpret_cast<const uint32_t *>(q);
                         else
-                            next.b[k][i] = (c < p.R ? bits_of(q[0]) : 0u) |
-                                           (c + 1 < p.R ? bits_of(q[1]) << 16 : 0u);
+                            next[k][i] = (c < p.R ? bits_of(q[0]) : 0u) |
+                                         (c + 1 < p.R ? bits_of(q[1]) << 16 : 0u);
                     }
                 }
         } else if constexpr (kAhead) {
@@ -266,11 +279,31 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = i & 1 ? r1 : r0, c = k * 8 + (i >> 1) * 4 + j;
-                    next.b[k][i] = on && row < p.M && c < p.R ? bits_of(b[(int64_t)row * p.R + c]) : 0;
+                    next[k][i] = m < m_last && row < p.M && c < p.R
+                                     ? bits_of(b[(int64_t)row * p.R + c]) : 0;
                 }
         }
     };
-    fetch_rows(m_first + (warp & 1));
+    // and of y kDepth tiles are: a lane copies what it will use itself
+    constexpr int kDepth = G::kDepth;
+    T *ring = reinterpret_cast<T *>(smem + G::kV) + warp * (kDepth * 512) + lane * 8;
+    const int64_t y_half = 8 * (int64_t)p.P, y_step = 32 * (int64_t)p.P;
+    const T *y_next = y + (int64_t)(m_own * 16 + g) * p.P + at;
+    int row_next = m_own * 16 + g;
+    auto fetch_y = [&](int slot) {
+        if (p.vec_y && row_next - g < m_last * 16) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int k = 0; k < 8; k += G::kVec) {
+                    const bool on = row_next + 8 * r < p.M && at + k < p.P;
+                    copy16(ring + slot * 512 + r * 256 + k, on ? y_next + r * y_half + k : y, on);
+                }
+        }
+        y_next += y_step;
+        row_next += 32;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 
     // v = a x over this block's channels; a warp has 16 of the positions
     {
@@ -346,6 +379,9 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
+        fetch_b(m_own);
+#pragma unroll
+        for (int k = 0; k < kDepth; ++k) fetch_y(k);
         // rows behind R are zero whatever x holds
 #pragma unroll
         for (int r = 0; r < RT; ++r)
@@ -415,10 +451,29 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
                 }
             }
         }
-    for (int m = m_first + (warp & 1); m < m_last; m += 2) {
+    int slot = 0;
+    T *o = out + (int64_t)(m_own * 16 + g) * p.P + at;
+    for (int m = m_own; m < m_last; m += 2, o += y_step) {
         const int r0 = m * 16 + g, r1 = r0 + 8;
-        Next now = next;
-        fetch_rows(m + 2);
+        Eight<T> e0, e1;
+        if (p.vec_y) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            e0.read(ring + slot * 512);
+            e1.read(ring + slot * 512 + 256);
+        } else {
+            e0.load(y + (int64_t)r0 * p.P, at, r0 < p.M ? p.P : 0, false);
+            e1.load(y + (int64_t)r1 * p.P, at, r1 < p.M ? p.P : 0, false);
+        }
+        uint32_t now[kPairs ? RT : kAhead ? 2 * RT : 1][4];
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int k = 0; k < (kPairs ? RT : 2 * RT); ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) now[k][i] = next[k][i];
+        }
+        fetch_b(m + 2);
+        fetch_y(slot);
+        slot = slot + 1 < kDepth ? slot + 1 : 0;
         float acc[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -429,8 +484,8 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
             for (int k = 0; k < RT; ++k) {
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    mma16<T>(acc[t], now.b[k], vl[k][t][0], vl[k][t][1]);
-                    mma16<T>(acc[t], now.b[k], vh[k][t][0], vh[k][t][1]);
+                    mma16<T>(acc[t], now[k], vl[k][t][0], vl[k][t][1]);
+                    mma16<T>(acc[t], now[k], vh[k][t][0], vh[k][t][1]);
                 }
             }
         } else {
@@ -440,7 +495,7 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int row = i & 1 ? r1 : r0, c = k * 8 + (i >> 1) * 4 + j;
-                    const float f = kAhead ? __uint_as_float(now.b[kAhead ? k : 0][i])
+                    const float f = kAhead ? __uint_as_float(now[kAhead ? k : 0][i])
                                     : row < p.M && c < p.R ? to_f32(b[(int64_t)row * p.R + c]) : 0.f;
                     split_tf32(f, bh[i], bl[i]);
                 }
@@ -458,11 +513,11 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float up = kHalf ? scale * unit[2 * t + i] : scale;
-                f0[2 * t + i] = fmaf(up, acc[t][i], now.e0.get(2 * t + i));
-                f1[2 * t + i] = fmaf(up, acc[t][2 + i], now.e1.get(2 * t + i));
+                f0[2 * t + i] = fmaf(up, acc[t][i], e0.get(2 * t + i));
+                f1[2 * t + i] = fmaf(up, acc[t][2 + i], e1.get(2 * t + i));
             }
-        if (r0 < p.M) now.e0.store(f0, out + (int64_t)r0 * p.P, at, p.P, p.vec_y);
-        if (r1 < p.M) now.e1.store(f1, out + (int64_t)r1 * p.P, at, p.P, p.vec_y);
+        if (r0 < p.M) e0.store(f0, o, 0, p.P - at, p.vec_y);
+        if (r1 < p.M) e1.store(f1, o + y_half, 0, p.P - at, p.vec_y);
     }
 }
 

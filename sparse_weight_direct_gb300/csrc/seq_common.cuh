@@ -89,7 +89,7 @@ struct alignas(V * sizeof(T) >= 16 ? 16 : V * sizeof(T)) Run {
     }
 };
 
-// row[t0, t0 + V) where t < end, zeros behind (positions behind `end` are not
+// row[t0, t0 + V) of global memory where t < end, zeros behind (positions behind `end` are not
 // read unless the run is whole, so what lies there does not matter).
 // vec: the run's address is aligned to the run.
 template <typename T, int V>
