@@ -221,17 +221,23 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
     const int half = p0 + (warp >> 1) * 32, at = half + j * 8;
     if (id < 0) {  // the same for the whole cluster
         if (static_cast<const void *>(out) == y) return;
-        for (int m = m_first + (warp & 1); m < m_last; m += 2)
-            for (int k = 0; k < 2; ++k) {
-                const int row = m * 16 + g + 8 * k;
-                if (row >= p.M) continue;
-                Eight<T> e;
-                e.load(y + (int64_t)row * p.P, at, p.P, p.vec_y);
-                float f[8];
+        constexpr int V = G::kVec, kRow = kPos / V, kBatch = 8;  // reads under way at once
+        const int row_end = min(p.M, m_last * 16), pieces = (row_end - m_first * 16) * kRow;
+        for (int i0 = threadIdx.x; i0 < pieces; i0 += kThreads * kBatch) {
+            Run<T, V> r[kBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = e.get(i);
-                e.store(f, out + (int64_t)row * p.P, at, p.P, p.vec_y);
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kThreads, row = m_first * 16 + i / kRow;
+                load_run(r[k], y + (int64_t)row * p.P, p0 + i % kRow * V, i < pieces ? p.P : 0,
+                         p.vec_y);
             }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kThreads, row = m_first * 16 + i / kRow;
+                store_run(r[k], out + (int64_t)row * p.P, p0 + i % kRow * V, i < pieces ? p.P : 0,
+                          p.vec_y);
+            }
+        }
         return;
     }
     const T *x = static_cast<const T *>(p.x) + n * p.x_sn;
@@ -645,12 +651,7 @@ int check_sizes(const spconv_adapter_args *a) {
 int launch_clusters(void (*fn)(AdapterParams), int64_t jobs, int ranks, int threads, int smem,
                     const AdapterParams &p, cudaStream_t stream) {
     if (jobs * ranks > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-        cudaGetLastError();
-        return SPCONV_ERR_CUDA;
-    }
+    if (int rc = raise_smem(reinterpret_cast<const void *>(fn), smem)) return rc;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(jobs * ranks));
     cfg.blockDim = dim3(threads);
@@ -726,7 +727,7 @@ SPCONV_API int spconv_adapter_add(const spconv_adapter_args *a, void *stream) {
     p.vec_y = rows_aligned(a->y, 0, a->P, e) && rows_aligned(a->out, 0, a->P, e);
     p.vec_b = aligned(a->b, 4) && a->R % 2 == 0;
     const int64_t jobs = (int64_t)p.N * p.tiles;
-    const int ranks = ranks_for(p, jobs, 4 * kSMs, 64);
+    const int ranks = ranks_for(p, jobs, 2 * kSMs, 64);
     return by_dtype(a->dtype, [&](auto t) {
         using T = decltype(t);
         auto go = [&](auto rt) {

@@ -10,7 +10,9 @@
 #include <cstddef>
 #include <cstdint>
 #include <initializer_list>
+#include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "spconv.h"
 
@@ -236,6 +238,26 @@ inline int by_dtype(int dtype, F f) {
         case SPCONV_F16: return f(__half{});
     }
     return SPCONV_ERR_INVALID_ARG;
+}
+
+// Allows a kernel `bytes` of dynamic shared memory, once per kernel and device
+// (a call per launch costs host time, and a launch may be under capture).
+inline int raise_smem(const void *fn, int bytes) {
+    if (bytes <= 48 * 1024) return SPCONV_OK;
+    static std::mutex lock;
+    static std::pair<const void *, int> done[256];
+    static int count = 0;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return SPCONV_ERR_CUDA;
+    std::lock_guard<std::mutex> hold(lock);
+    for (int i = 0; i < count; ++i)
+        if (done[i].first == fn && done[i].second == device) return SPCONV_OK;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return SPCONV_ERR_CUDA;
+    }
+    if (count < 256) done[count++] = {fn, device};
+    return SPCONV_OK;
 }
 
 inline int launch_status() {

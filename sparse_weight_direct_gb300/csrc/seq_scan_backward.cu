@@ -442,12 +442,7 @@ SPCONV_API int spconv_scan_backward(const spconv_scan_args *a, void *stream) {
             if (int rc = launch_status()) return rc;
             if (int rc = scan_join_chunks(p, true, s)) return rc;
             auto *fn = gradient_kernel<T, SPT>;
-            if (cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     smem) != cudaSuccess) {
-                cudaGetLastError();
-                return (int)SPCONV_ERR_CUDA;
-            }
+            if (int rc = raise_smem(reinterpret_cast<const void *>(fn), smem)) return rc;
             fn<<<dim3(grid.x, grid.y, p.segments), kScanThreads, smem, s>>>(p);
             if (int rc = launch_status()) return rc;
             join_weights_kernel<<<(unsigned)((weights + 255) / 256), 256, 0, s>>>(p);
