@@ -298,47 +298,48 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanParams p) {
     }
 }
 
-// Joins the chunks in their order: on entry h_chunk holds the state that each
-// chunk leaves from a zero state (and g_chunk the gradient that reaches its
+// Joins chunks in their order: on entry h_chunk holds the state that each
+// leaves from a zero state (blocks y = 1: g_chunk the gradient that reaches its
 // start from its own outputs), on return the state that it starts from (the
 // gradient of the state that it leaves).  A chunk's decay is e^(A sum dt).
 // Eight chunks are read at a time, so that the reads do not wait for the
 // writes before them.
-__global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, int grad) {
+__global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, int h_chunks,
+                                                          int g_chunks) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t per = (int64_t)p.channels * p.S;
     if (i >= p.N * per) return;
+    const bool back = blockIdx.y;
+    const int chunks = back ? g_chunks : h_chunks;
     const int n = (int)(i / per);
     const int64_t cs = i - n * per;
     const float A = p.A[cs] * kLog2e;
-    const int64_t base = (int64_t)n * p.chunks;
-    const float *dts = p.dt_chunk + base * p.channels + cs / p.S;
+    const int64_t base = (int64_t)n * chunks;
+    const float *dts = (back ? p.dt_segment : p.dt_chunk) + base * p.channels + cs / p.S;
+    float *rows = (back ? p.g_chunk : p.h_chunk) + base * per + cs;
+    const float *first = back ? p.dfinal : p.state;
+    float v = first ? first[i] : 0.f;
     constexpr int kBatch = 8;
-    for (int back = 0; back <= grad; ++back) {
-        float *rows = (back ? p.g_chunk : p.h_chunk) + base * per + cs;
-        const float *first = back ? p.dfinal : p.state;
-        float v = first ? first[i] : 0.f;
-        for (int k0 = 0; k0 < p.chunks; k0 += kBatch) {
-            float left[kBatch], decay[kBatch];
+    for (int k0 = 0; k0 < chunks; k0 += kBatch) {
+        float left[kBatch], decay[kBatch];
 #pragma unroll
-            for (int e = 0; e < kBatch; ++e) {
-                const int k = back ? p.chunks - 1 - k0 - e : k0 + e;
-                if (k0 + e < p.chunks) {
-                    left[e] = rows[k * per];
-                    decay[e] = dts[(int64_t)k * p.channels];
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < kBatch; ++e) {
-                const int k = back ? p.chunks - 1 - k0 - e : k0 + e;
-                if (k0 + e < p.chunks) {
-                    rows[k * per] = v;
-                    v = fmaf(ex2(A * decay[e]), v, left[e]);
-                }
+        for (int e = 0; e < kBatch; ++e) {
+            const int k = back ? chunks - 1 - k0 - e : k0 + e;
+            if (k0 + e < chunks) {
+                left[e] = rows[k * per];
+                decay[e] = dts[(int64_t)k * p.channels];
             }
         }
-        if (back && p.dstate) p.dstate[i] = v;
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            const int k = back ? chunks - 1 - k0 - e : k0 + e;
+            if (k0 + e < chunks) {
+                rows[k * per] = v;
+                v = fmaf(ex2(A * decay[e]), v, left[e]);
+            }
+        }
     }
+    if (back && p.dstate) p.dstate[i] = v;
 }
 
 // Step: four lanes per request and channel, as in the scan; the states are
@@ -414,9 +415,8 @@ ScanParams scan_params(const spconv_scan_args *a) {
     p.c_sn = a->c_stride_n; p.c_sg = a->c_stride_g; p.c_ss = a->c_stride_s;
     p.N = a->N; p.channels = a->channels; p.L = a->L; p.S = a->S; p.groups = a->groups;
     p.per_group = a->channels / a->groups;
-    p.blocks_per_group = (p.per_group + kScanChannels - 1) / kScanChannels;
     p.softplus = a->softplus; p.num_slots = a->num_slots;
-    p.chunks = p.segments = p.chunks_per_segment = 1;
+    p.chunks = 1;
     p.chunk_len = a->L;
     p.vec = rows_aligned(a->u, p.u_sn, p.u_sc, e) && rows_aligned(a->delta, p.d_sn, p.d_sc, e) &&
             (!a->z || rows_aligned(a->z, p.z_sn, p.z_sc, e)) &&
@@ -428,7 +428,8 @@ ScanParams scan_params(const spconv_scan_args *a) {
 
 int scan_join_chunks(const ScanParams &p, bool grad, cudaStream_t stream) {
     const int64_t count = (int64_t)p.N * p.channels * p.S;
-    join_chunks_kernel<<<(unsigned)((count + 255) / 256), 256, 0, stream>>>(p, grad);
+    join_chunks_kernel<<<dim3((unsigned)((count + 255) / 256), grad ? 2 : 1), 256, 0, stream>>>(
+        p, grad ? p.tiles : p.chunks, p.segments);
     return launch_status();
 }
 

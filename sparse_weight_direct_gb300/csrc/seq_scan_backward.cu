@@ -7,102 +7,226 @@
 //   q_t = a_t g_t h_(t-1),  ddt = u (g_t . B_t) + sum_s q_t A,  dA = sum q_t dt
 //   du = dt (g_t . B_t) + D do_t,  dD = sum do_t u,  ddelta = ddt sigmoid(raw)
 //
-// Both recurrences are cut into chunks of one tile.  One kernel finds what
-// every chunk leaves of h from zero and of g towards its start; one joins the
-// chunks over the sequence; one forms every chunk's gradients from the states
-// that it starts and ends with, its h_t held in shared memory between its run
-// forwards and its run back.  So all chunks run side by side and no state is
-// kept by the forward call: the states cost two numbers per chunk of
-// traffic, not one per position.  Sums over channels, sequences and chunks
-// are joined from the blocks' shares in a fixed order.
-#include <utility>
-
+// The sequence is cut into tiles of 32 positions and segments of a few tiles.
+// One kernel finds what every tile leaves of h from zero and every segment of g
+// towards its start; one joins them over the sequence; one forms every
+// segment's gradients from the states that its tiles start with and the
+// gradient that it ends with.  So all segments run side by side and nothing is
+// kept by the forward call: the states cost a number per tile of traffic, not
+// one per position.  Within a tile the gradient kernel runs forwards once, keeping
+// the states before every fourth position in shared memory, and then goes back
+// by four positions at a time: their states and decays are formed again, in
+// registers, and used up backwards.  An exponential three times per state
+// and position in all is cheaper than the traffic of keeping it.
+// Sums over channels, sequences and segments are joined from the blocks' shares
+// in a fixed order.
 #include "seq_scan.cuh"
 
 namespace spconv {
 namespace seq {
 namespace {
 
-// Positions of a lane in a tile: the tile's h_t, 32 channels of 4 * SPT states,
-// have to fit shared memory.
-constexpr int run_of(int SPT) { return SPT <= 4 ? 8 : SPT == 8 ? 4 : 2; }
+constexpr int kBackThreads = 128, kBackWarps = kBackThreads / 32;
 
-template <int SPT>
+// A block owns 64 channels of one group of one sequence, a warp 16 of them, four
+// lanes a pair of channels with SPT states of each in every lane: what is
+// read of B and C serves two channels (see seq_scan.cu), and the registers
+// hold four positions' states and decays.
+template <int SPT_>
 struct BackTile {
-    static constexpr int VE = run_of(SPT), TT = 4 * VE, SP = 4 * SPT;
-    // words of one position's states; 16 more than the channels need, so that
-    // neighbouring positions start in different banks
-    static constexpr int kHRow = kScanChannels * SP + 16;
-    static constexpr int kPitch = TT + 4;
+    static constexpr int SPT = SPT_, SP = 4 * SPT, NP = Pairs<SPT>::N;
+    static constexpr int VE = SPT <= 4 ? 8 : SPT == 8 ? 4 : 2, TT = 4 * VE;
+    static constexpr int Q = SPT <= 4 ? 4 : SPT == 8 ? 2 : 1;  // positions gone back at a time
+    static constexpr int CW = 16, CB = CW * kBackWarps;        // channels of a warp, of a block
+    static constexpr int NI = 2;  // loads of a lane from each row set
+    static constexpr int NB = (2 * SP * 4 + kBackThreads - 1) / kBackThreads;  // from B and C
+    // rows: one more after every VE positions, pitches that keep the writers of
+    // a position's row and the pairs that read it in different banks
+    static constexpr int kStepPitch = TT + 10;  // of 16 bytes {dt, dt u} of a pair
+    static constexpr int kDoPitch = TT + 5;     // of 8 bytes {do} of a pair
+    static constexpr int kOutPitch = TT + 4;
+    static constexpr int kOutHalf = 8 * kOutPitch + 8, kOut = 2 * kOutHalf;
+    static constexpr int kKept = 2 * NP * 32 * 2;  // floats: a warp's states before Q positions
+    // floats of a block
+    static constexpr int kMatrix = (TT + 5) * SP;
+    static constexpr int kBC = 2 * kMatrix;
+    static constexpr int kSteps = 8 * kStepPitch * 4;  // of a warp, from here
+    static constexpr int kDo = 8 * kDoPitch * 2;
+    static constexpr int kKeptAll = TT / Q * kKept;
+    static constexpr int kOuts = 3 * kOut;
+    static constexpr int kWarp = kSteps + kDo + kKeptAll + kOuts;
+    static constexpr int kEnds = kBC + kBackWarps * (kSteps + kDo);
+    static constexpr int kAll = kBC + kBackWarps * kWarp;
+    static __device__ __forceinline__ int row(int t) { return t + t / VE; }
 };
 
-// What a chunk leaves: h from zero, the gradient of its start, its decay.
+// Where a thread works.
 template <typename T, int SPT>
-__global__ void __launch_bounds__(kScanThreads) chunk_ends_kernel(const ScanParams p) {
+struct BackPlace {
     using G = BackTile<SPT>;
-    constexpr int VE = G::VE, TT = G::TT, SP = G::SP;
-    __shared__ __align__(16) float bc[2 * TT * SP];
-    __shared__ __align__(16) float4 xs[kScanChannels][TT + 1];  // dt, dt u, do
-    const int ch = threadIdx.x >> 2, j = threadIdx.x & 3, s0 = j * SPT;
-    const int chunk = blockIdx.z;
-    const ScanPlace at(p, blockIdx.y, blockIdx.x);
-    const int t0 = chunk * TT;
-    const int end = max(min(at.len, t0 + TT), t0), row_end = at.valid ? end : 0;
-    const int64_t slot = (int64_t)at.n * p.chunks + chunk;
-    float h[SPT], g[SPT];
+    static constexpr int VE = G::VE, TT = G::TT, SP = G::SP, NI = G::NI;
+    const ScanParams &p;
+    int n, g, len, lane, warp, quarter, c_count;
+    int64_t c_base;  // the warp's first channel
+    const T *u, *d, *z, *dy, *B, *C;
+    float bias[NI];
+    float *bc, *steps, *dos;
+    Run<T, VE> ru[NI], rd[NI], rz[NI], ry[NI];
+
+    __device__ BackPlace(const ScanParams &p_, float *sm) : p(p_) {
+        n = blockIdx.y;
+        g = blockIdx.x / p.blocks_per_group;
+        lane = threadIdx.x & 31;
+        warp = threadIdx.x >> 5;
+        quarter = lane & 3;
+        const int first = (blockIdx.x - g * p.blocks_per_group) * G::CB + warp * G::CW;
+        c_count = min(max(p.per_group - first, 0), G::CW);
+        c_base = (int64_t)g * p.per_group + min(first, p.per_group - 1);
+        len = p.lengths ? min(max(p.lengths[n], 0), p.L) : p.L;
+        u = static_cast<const T *>(p.u) + n * p.u_sn + c_base * p.u_sc;
+        d = static_cast<const T *>(p.delta) + n * p.d_sn + c_base * p.d_sc;
+        z = p.z ? static_cast<const T *>(p.z) + n * p.z_sn + c_base * p.z_sc : nullptr;
+        dy = static_cast<const T *>(p.dy) + n * p.dy_sn + c_base * p.dy_sc;
+        B = static_cast<const T *>(p.B) + n * p.b_sn + g * p.b_sg;
+        C = static_cast<const T *>(p.C) + n * p.c_sn + g * p.c_sg;
+        bc = sm;
+        steps = sm + G::kBC + warp * (G::kSteps + G::kDo);
+        dos = steps + G::kSteps;
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) h[i] = g[i] = 0.f;
-    float total = 0.f;
-    if (t0 < end) {
-        const T *ur = static_cast<const T *>(p.u) + at.n * p.u_sn + at.c * p.u_sc;
-        const T *dr = static_cast<const T *>(p.delta) + at.n * p.d_sn + at.c * p.d_sc;
-        const T *zr = p.z ? static_cast<const T *>(p.z) + at.n * p.z_sn + at.c * p.z_sc : nullptr;
-        const T *yr = static_cast<const T *>(p.dy) + at.n * p.dy_sn + at.c * p.dy_sc;
-        Run<T, VE> u, d, z, dy;
-        load_run(u, ur, t0 + j * VE, row_end, p.vec);
-        load_run(d, dr, t0 + j * VE, row_end, p.vec);
-        load_run(dy, yr, t0 + j * VE, row_end, p.vec);
-        if (zr) load_run(z, zr, t0 + j * VE, row_end, p.vec);
-        ScanBC<T, SPT, VE> rows;
-        rows.load(p, at, t0, end);
-        const float bias = p.delta_bias ? p.delta_bias[at.c] : 0.f;
-        float A[SPT], P[SPT];
-        load_states<SPT>(A, p.A + (int64_t)at.c * p.S, s0, p.S);
+        for (int k = 0; k < NI; ++k)
+            bias[k] = p.delta_bias && lane / 4 + 8 * k < c_count ? p.delta_bias[c_base + lane / 4 + 8 * k]
+                                                                 : 0.f;
+    }
+    // Reads a tile's rows and leaves B, C, {dt, dt u} and do in shared memory;
+    // behind the sequence's end, and for channels that do not exist, all are zero.
+    // total: the step sizes' sums of the lane's positions.
+    __device__ __forceinline__ void stage(int t0, float (&total)[NI]) {
+        const int end = min(len, min(p.L - t0, TT) + t0), mine = t0 + quarter * VE;
+        Run<T, VE> rows[G::NB];
 #pragma unroll
-        for (int i = 0; i < SPT; ++i) {
-            A[i] *= kLog2e;
-            P[i] = 1.f;
+        for (int k = 0; k < NI; ++k) {
+            const int c = lane / 4 + 8 * k, e = c < c_count ? end : 0;
+            load_run(ru[k], u + c * p.u_sc, mine, e, p.vec);
+            load_run(rd[k], d + c * p.d_sc, mine, e, p.vec);
+            load_run(ry[k], dy + c * p.dy_sc, mine, e, p.vec);
+            if (z) load_run(rz[k], z + c * p.z_sc, mine, e, p.vec);
         }
-        rows.store(bc);
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            const float dt = t0 + j * VE + e < row_end ? step_size(p, d[e] + bias) : 0.f;
-            float o = dy[e];
-            if (zr) o *= silu(z[e]);
-            xs[ch][j * VE + e] = make_float4(dt, dt * u[e], o, 0.f);
+        for (int k = 0; k < G::NB; ++k) {
+            const int i = threadIdx.x + kBackThreads * k, s = i % SP, q = (i / SP) % 4;
+            const int which = i / (SP * 4);
+            const T *row = which ? C + s * p.c_ss : B + s * p.b_ss;
+            load_run(rows[k], row, t0 + q * VE, s < p.S && which < 2 ? end : 0, p.vec);
         }
-        __syncthreads();
-#pragma unroll 4
-        for (int t = 0; t < TT; ++t) {
-            const float4 x = xs[ch][t];
-            total += x.x;
-            float b[SPT], c[SPT];
-            read_states<SPT>(b, bc + t * SP + s0);
-            read_states<SPT>(c, bc + (TT + t) * SP + s0);
+        __syncthreads();  // the previous tile has been read
 #pragma unroll
-            for (int i = 0; i < SPT; ++i) {
-                const float a = ex2(x.x * A[i]);
-                h[i] = fmaf(a, h[i], x.y * b[i]);
-                P[i] *= a;
-                g[i] = fmaf(P[i] * c[i], x.z, g[i]);
+        for (int k = 0; k < G::NB; ++k) {
+            const int i = threadIdx.x + kBackThreads * k, s = i % SP, q = (i / SP) % 4;
+            const int which = i / (SP * 4);
+            if (which >= 2) break;
+            float *to = bc + which * G::kMatrix + q * (VE + 1) * SP + s;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) to[e * SP] = rows[k][e];
+        }
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            const int c = lane / 4, first = quarter * (VE + 1);
+            float dt[VE], o[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                dt[e] = rd[k][e] + bias[k];
+                o[e] = ry[k][e];
+            }
+            if (p.softplus) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) dt[e] = softplus(dt[e]);
+            }
+            if (z) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) o[e] *= silu(rz[k][e]);
+            }
+            const bool on = c + 8 * k < c_count;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                dt[e] = on && mine + e < end ? dt[e] : 0.f;
+                total[k] += dt[e];
+                reinterpret_cast<float2 *>(steps)[(c * G::kStepPitch + first + e) * 2 + k] =
+                    make_float2(dt[e], dt[e] * ru[k][e]);
+                dos[(c * G::kDoPitch + first + e) * 2 + k] = o[e];
             }
         }
+        __syncthreads();
     }
-    if (!at.valid) return;
-    const int64_t to = (slot * p.channels + at.c) * p.S;
-    store_states<SPT>(p.h_chunk + to, h, s0, p.S);
-    store_states<SPT>(p.g_chunk + to, g, s0, p.S);
-    if (j == 0) p.dt_chunk[slot * p.channels + at.c] = total;
+};
+
+// What a tile leaves of h from zero and a segment of g towards its start.
+template <typename T, int SPT>
+__global__ void __launch_bounds__(kBackThreads) segment_ends_kernel(const ScanParams p) {
+    using G = BackTile<SPT>;
+    constexpr int VE = G::VE, TT = G::TT, SP = G::SP, NP = G::NP, NI = G::NI;
+    extern __shared__ __align__(16) float sm[];
+    BackPlace<T, SPT> at(p, sm);
+    const int pair = at.lane >> 2, j = at.lane & 3, s0 = j * SPT, seg = blockIdx.z;
+    const float4 *step = reinterpret_cast<const float4 *>(at.steps) + pair * G::kStepPitch;
+    const float2 *dos = reinterpret_cast<const float2 *>(at.dos) + pair * G::kDoPitch;
+    Pairs<SPT> A[2], h[2], P[2], g[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int c = pair + 8 * q;
+        A[q].load(p.A + (at.c_base + c) * p.S, s0, c < at.c_count ? p.S : 0);
+        A[q].scale(kLog2e);
+        P[q].fill(1.f);
+        g[q].fill(0.f);
+    }
+    float all[NI] = {};
+    const int first = seg * p.tiles_per_segment, last = min(p.tiles, first + p.tiles_per_segment);
+    for (int tile = first; tile < last; ++tile) {
+        float total[NI] = {};
+        at.stage(tile * TT, total);
+        h[0].fill(0.f);
+        h[1].fill(0.f);
+#pragma unroll 4
+        for (int t = 0; t < TT; ++t) {
+            const float4 x = step[G::row(t)];
+            const float2 o = dos[G::row(t)];
+            Pairs<SPT> b, c;
+            b.read(at.bc + G::row(t) * SP + s0);
+            c.read(at.bc + G::kMatrix + G::row(t) * SP + s0);
+            const f32x2 dt[2] = {pack2(x.x, x.x), pack2(x.z, x.z)};
+            const f32x2 du[2] = {pack2(x.y, x.y), pack2(x.w, x.w)};
+            const f32x2 od[2] = {pack2(o.x, o.x), pack2(o.y, o.y)};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const f32x2 a = ex2_2(mul2(dt[q], A[q].v[i]));
+                    h[q].v[i] = fma2(a, h[q].v[i], mul2(du[q], b.v[i]));
+                    P[q].v[i] = mul2(P[q].v[i], a);
+                    g[q].v[i] = fma2(mul2(P[q].v[i], c.v[i]), od[q], g[q].v[i]);
+                }
+            }
+        }
+        const int64_t rows = ((int64_t)at.n * p.tiles + tile) * p.channels + at.c_base;
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            total[k] += __shfl_xor_sync(~0u, total[k], 1);
+            total[k] += __shfl_xor_sync(~0u, total[k], 2);
+            all[k] += total[k];
+            const int c = at.lane / 4 + 8 * k;
+            if (at.quarter == 0 && c < at.c_count) p.dt_chunk[rows + c] = total[k];
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (pair + 8 * q < at.c_count) h[q].store(p.h_chunk + (rows + pair + 8 * q) * p.S, s0, p.S);
+    }
+    const int64_t rows = ((int64_t)at.n * p.segments + seg) * p.channels + at.c_base;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int c = pair + 8 * q;
+        if (c >= at.c_count) continue;
+        g[q].store(p.g_chunk + (rows + c) * p.S, s0, p.S);
+        if (j == 0) p.dt_segment[rows + c] = all[q];
+    }
 }
 
 static __device__ __forceinline__ float sum4(float v) {
@@ -110,181 +234,276 @@ static __device__ __forceinline__ float sum4(float v) {
     return v + __shfl_xor_sync(~0u, v, 2);
 }
 
-// Shared memory of the gradient kernel, in floats.
-template <int SPT>
-constexpr int gradient_smem() {
-    using G = BackTile<SPT>;
-    return G::TT * G::kHRow + 2 * G::TT * G::SP + kScanChannels * (2 * (G::TT + 2) + 2 * G::kPitch);
-}
-
-// The gradients of a segment's chunks, last chunk first.
-template <typename T, int SPT>
-__global__ void __launch_bounds__(kScanThreads) gradient_kernel(const ScanParams p) {
-    using G = BackTile<SPT>;
-    constexpr int VE = G::VE, TT = G::TT, SP = G::SP;
-    extern __shared__ __align__(16) float sm[];
-    float *hb = sm;                       // [TT][kHRow]: h_t, then g_t
-    float *bc = hb + TT * G::kHRow;       // [2][TT][SP]
-    const int ch = threadIdx.x >> 2, j = threadIdx.x & 3, s0 = j * SPT;
-    float *dob_all = bc + 2 * TT * SP;    // [channel][kPitch]
-    float *dob = dob_all + ch * G::kPitch;
-    float *yb = dob_all + kScanChannels * G::kPitch + ch * G::kPitch;
-    float *dtu_all = dob_all + 2 * kScanChannels * G::kPitch;  // [channel][TT + 2] of {dt, dt u}
-    float2 *dtu = reinterpret_cast<float2 *>(dtu_all) + ch * (TT + 2);
-
-    const int cb = blockIdx.x, seg = blockIdx.z;
-    const ScanPlace at(p, blockIdx.y, cb);
-    const int64_t row = (int64_t)at.n * p.channels + at.c;
-    const T *ur = static_cast<const T *>(p.u) + at.n * p.u_sn + at.c * p.u_sc;
-    const T *dr = static_cast<const T *>(p.delta) + at.n * p.d_sn + at.c * p.d_sc;
-    const T *zr = p.z ? static_cast<const T *>(p.z) + at.n * p.z_sn + at.c * p.z_sc : nullptr;
-    const T *yr = static_cast<const T *>(p.dy) + at.n * p.dy_sn + at.c * p.dy_sc;
-    const float bias = p.delta_bias ? p.delta_bias[at.c] : 0.f, D = p.D ? p.D[at.c] : 0.f;
-    float A[SPT], dA[SPT], dD = 0.f, dbias = 0.f;
-    load_states<SPT>(A, p.A + (int64_t)at.c * p.S, s0, p.S);
+// Sums v[matrix][state] over the eight pairs of a warp (lane bits 4, 3, 2): at
+// each bit the lanes give half of what they hold to each other, states first,
+// then the matrices, so that every lane ends with its own share of the sums
+// (v[0 .. MATS)[0 .. N)), the first state of which is `state`, of matrix `mat`.
+template <int SPT, int MATS, int N, int BIT>
+struct PairSum {
+    static __device__ __forceinline__ void run(float (&v)[2][SPT], int lane, int &state, int &mat) {
+        if constexpr (BIT >= 4) {
+            const bool up = lane & BIT;
+            if constexpr (N > 1) {
 #pragma unroll
-    for (int i = 0; i < SPT; ++i) dA[i] = 0.f;
-
-    const int first = seg * p.chunks_per_segment;
-    const int last = min(p.chunks, first + p.chunks_per_segment) - 1;
-    for (int chunk = last; chunk >= first; --chunk) {
-        const int t0 = chunk * TT, stop = min(p.L, t0 + TT);
-        const int end = max(min(at.len, stop), t0), row_end = at.valid ? end : 0;
-        const int mine = t0 + j * VE;
-        const int64_t place = (((int64_t)at.n * p.chunks + chunk) * p.channels + at.c) * p.S;
-        Run<T, VE> u, d, z, dy;
-        load_run(u, ur, mine, row_end, p.vec);
-        load_run(d, dr, mine, row_end, p.vec);
-        load_run(dy, yr, mine, row_end, p.vec);
-        if (zr) load_run(z, zr, mine, row_end, p.vec);
-        ScanBC<T, SPT, VE> rows;
-        rows.load(p, at, t0, end);
-        float h0[SPT], g[SPT], h[SPT];
-        load_states<SPT>(h0, p.h_chunk + place, s0, at.valid ? p.S : 0);
-        load_states<SPT>(g, p.g_chunk + place, s0, at.valid ? p.S : 0);
-        __syncthreads();  // the previous chunk's last reads of shared memory
-        rows.store(bc);
+                for (int w = 0; w < MATS; ++w)
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            const float dt = mine + e < row_end ? step_size(p, d[e] + bias) : 0.f;
-            float o = dy[e];
-            if (zr) o *= silu(z[e]);
-            dtu[j * VE + e] = make_float2(dt, dt * u[e]);
-            dob[j * VE + e] = o;
-            dD = fmaf(o, u[e], dD);
-        }
-        __syncthreads();
-        // forwards: h_t of every position, and o without D u
-#pragma unroll
-        for (int i = 0; i < SPT; ++i) h[i] = h0[i];
-        float *mine_h = hb + ch * SP + s0;
-#pragma unroll 4
-        for (int t = 0; t < TT; ++t) {
-            const float2 x = dtu[t];
-            float b[SPT], c[SPT], o = 0.f;
-            read_states<SPT>(b, bc + t * SP + s0);
-            read_states<SPT>(c, bc + (TT + t) * SP + s0);
-#pragma unroll
-            for (int i = 0; i < SPT; ++i) {
-                h[i] = fmaf(ex2(x.x * (A[i] * kLog2e)), h[i], x.y * b[i]);
-                o = fmaf(h[i], c[i], o);
-            }
-            write_states<SPT>(mine_h + t * G::kHRow, h);
-            o = sum4(o);
-            if (j == 0) yb[t] = o;
-        }
-        __syncthreads();
-        // dz, and this block's share of dC
-        if (zr) {
-            float w[VE];
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float o = fmaf(D, u[e], yb[j * VE + e]);
-                w[e] = mine + e < end ? dy[e] * o * silu_grad(z[e]) : 0.f;
-            }
-            Run<T, VE> out;
-            out.put(w);
-            if (at.valid) store_run(out, static_cast<T *>(p.dz) + row * p.L, mine, stop, p.vec_y);
-        }
-        // over = the sum over the block's channels of w(channel, t) * hb[t][channel][s]
-        auto over_channels = [&](auto w, int which) {
-            const int64_t base = ((((int64_t)which * gridDim.x + cb) * p.N + at.n) * p.L + t0) * p.S;
-            for (int i = threadIdx.x; i < TT * SP; i += kScanThreads) {
-                const int t = i / SP, s = i % SP;
-                float v = 0.f;
-#pragma unroll 8
-                for (int k = 0; k < kScanChannels; ++k)
-                    v = fmaf(w(k, t), hb[t * G::kHRow + k * SP + s], v);
-                if (s < p.S && t0 + t < stop) p.part_bc[base + (int64_t)t * p.S + s] = v;
-            }
-        };
-        over_channels([&](int k, int t) { return dob_all[k * G::kPitch + t]; }, 1);
-        __syncthreads();
-        // back: g_t in the place of h_t
-        float sums[2][VE];  // of the lane's own positions: g . B and q . A
-#pragma unroll
-        for (int t = TT - 1; t >= 0; --t) {
-            const float2 x = dtu[t];
-            const float o = dob[t];
-            float b[SPT], c[SPT], before[SPT], sb = 0.f, sa = 0.f;
-            read_states<SPT>(b, bc + t * SP + s0);
-            read_states<SPT>(c, bc + (TT + t) * SP + s0);
-            if (t > 0)
-                read_states<SPT>(before, mine_h + (t - 1) * G::kHRow);
-            else
-#pragma unroll
-                for (int i = 0; i < SPT; ++i) before[i] = h0[i];
-            float now[SPT];
-#pragma unroll
-            for (int i = 0; i < SPT; ++i) {
-                now[i] = fmaf(c[i], o, g[i]);
-                sb = fmaf(now[i], b[i], sb);
-                g[i] = now[i] * ex2(x.x * (A[i] * kLog2e));
-                const float q = g[i] * before[i];
-                sa = fmaf(q, A[i], sa);
-                dA[i] = fmaf(q, x.x, dA[i]);
-            }
-            write_states<SPT>(mine_h + t * G::kHRow, now);
-            sb = sum4(sb);
-            sa = sum4(sa);
-            if (t / VE == j) {
-                sums[0][t % VE] = sb;
-                sums[1][t % VE] = sa;
+                    for (int i = 0; i < N / 2; ++i) {
+                        const float keep = up ? v[w][i + N / 2] : v[w][i];
+                        const float give = up ? v[w][i] : v[w][i + N / 2];
+                        v[w][i] = keep + __shfl_xor_sync(~0u, give, BIT);
+                    }
+                state += up ? N / 2 : 0;
+                PairSum<SPT, MATS, N / 2, BIT / 2>::run(v, lane, state, mat);
+            } else if constexpr (MATS > 1) {
+                const float keep = up ? v[1][0] : v[0][0], give = up ? v[0][0] : v[1][0];
+                v[0][0] = keep + __shfl_xor_sync(~0u, give, BIT);
+                mat = up;
+                PairSum<SPT, 1, 1, BIT / 2>::run(v, lane, state, mat);
+            } else {
+                v[0][0] += __shfl_xor_sync(~0u, v[0][0], BIT);
+                PairSum<SPT, 1, 1, BIT / 2>::run(v, lane, state, mat);
             }
         }
-        {
-            float wu[VE], wd[VE];
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float raw = d[e] + bias, uu = u[e];
-                const float dt = dtu[j * VE + e].x;
-                const bool in = mine + e < end;
-                float ddt = fmaf(sums[0][e], uu, sums[1][e]);
-                if (p.softplus) ddt *= sigmoid(raw);
-                ddt = in ? ddt : 0.f;
-                dbias += at.valid ? ddt : 0.f;
-                wd[e] = ddt;
-                wu[e] = in ? fmaf(sums[0][e], dt, D * dob[j * VE + e]) : 0.f;
-            }
-            Run<T, VE> du, dd;
-            du.put(wu);
-            dd.put(wd);
-            if (at.valid) {
-                store_run(du, static_cast<T *>(p.du) + row * p.L, mine, stop, p.vec_y);
-                store_run(dd, static_cast<T *>(p.ddelta) + row * p.L, mine, stop, p.vec_y);
-            }
-        }
-        __syncthreads();
-        over_channels([&](int k, int t) { return dtu_all[(k * (TT + 2) + t) * 2 + 1]; }, 0);
     }
-    dD = sum4(dD);
-    dbias = sum4(dbias);
-    if (!at.valid) return;
-    float *to = p.part_a + (((int64_t)at.n * p.segments + seg) * p.channels + at.c) * (p.S + 2);
-    store_states<SPT>(to, dA, s0, p.S);
-    if (j == 0) {
-        to[p.S] = dD;
-        to[p.S + 1] = dbias;
+};
+template <int SPT>
+struct PairShare {  // what PairSum leaves in a lane
+    static constexpr int N = SPT >= 8 ? SPT / 8 : 1, MATS = SPT >= 8 ? 2 : 1;
+};
+
+// The gradients of a segment's tiles, last tile first.
+template <typename T, int SPT>
+__global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams p) {
+    using G = BackTile<SPT>;
+    constexpr int VE = G::VE, TT = G::TT, SP = G::SP, NP = G::NP, NI = G::NI, Q = G::Q;
+    constexpr float kLn2 = 0.6931471805599453f;
+    extern __shared__ __align__(16) float sm[];
+    BackPlace<T, SPT> at(p, sm);
+    const int lane = at.lane, pair = lane >> 2, j = lane & 3, s0 = j * SPT, odd = j & 1;
+    float *kept_all = sm + G::kBC + kBackWarps * (G::kSteps + G::kDo);
+    float *kept = kept_all + at.warp * G::kKeptAll;
+    float *outs = kept_all + kBackWarps * G::kKeptAll + at.warp * G::kOuts;
+    // Odd lanes hold the pair's channels the other way round: in a sum over two
+    // lanes every lane keeps its first and gives its second.
+    const int mine[2] = {pair + 8 * odd, pair + 8 * (odd ^ 1)};
+    const float2 *step[2];
+    const float *dos[2];
+    Pairs<SPT> A[2], dA[2], g[2];
+    const int seg = blockIdx.z;
+    const int64_t seg_rows = ((int64_t)at.n * p.segments + seg) * p.channels + at.c_base;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int S = mine[q] < at.c_count ? p.S : 0;
+        A[q].load(p.A + (at.c_base + mine[q]) * p.S, s0, S);
+        A[q].scale(kLog2e);
+        g[q].load(p.g_chunk + (seg_rows + mine[q]) * p.S, s0, S);
+        dA[q].fill(0.f);
+        step[q] = reinterpret_cast<const float2 *>(at.steps) + pair * G::kStepPitch * 2 + (odd ^ q);
+        dos[q] = at.dos + pair * G::kDoPitch * 2 + (odd ^ q);
+    }
+    float D[NI], dD[NI] = {}, dbias[NI] = {};
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+        const int c = lane / 4 + 8 * k;
+        D[k] = p.D && c < at.c_count ? p.D[at.c_base + c] : 0.f;
+    }
+    const int first = seg * p.tiles_per_segment, last = min(p.tiles, first + p.tiles_per_segment);
+    const int64_t rows = (int64_t)at.n * p.channels + at.c_base;
+    for (int tile = last - 1; tile >= first; --tile) {
+        const int t0 = tile * TT;
+        float unused[NI] = {};
+        Pairs<SPT> h[2];
+        const int64_t tile_rows = ((int64_t)at.n * p.tiles + tile) * p.channels + at.c_base;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            h[q].load(p.h_chunk + (tile_rows + mine[q]) * p.S, s0, mine[q] < at.c_count ? p.S : 0);
+        at.stage(t0, unused);
+        // forwards: the states before every Q positions
+#pragma unroll 1
+        for (int m = 0; m < TT / Q; ++m) {
+            f32x2 *to = reinterpret_cast<f32x2 *>(kept + m * G::kKept) + lane;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) to[(q * NP + i) * 32] = h[q].v[i];
+            if (m == TT / Q - 1) break;
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                const int r = G::row(m * Q) + k;  // (Q divides VE)
+                Pairs<SPT> b;
+                b.read(at.bc + r * SP + s0);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float2 x = step[q][r * 2];
+                    const f32x2 dt = pack2(x.x, x.x), du = pack2(x.y, x.y);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        h[q].v[i] = fma2(ex2_2(mul2(dt, A[q].v[i])), h[q].v[i], mul2(du, b.v[i]));
+                }
+            }
+        }
+        // back, Q positions at a time
+#pragma unroll 1
+        for (int m = TT / Q - 1; m >= 0; --m) {
+            const int r0 = G::row(m * Q);
+            f32x2 hs[Q + 1][2][NP], a[Q][2][NP];
+            Pairs<SPT> b[Q], c[Q];
+            float2 x[Q][2];
+            float y[Q][2];
+            const f32x2 *from = reinterpret_cast<const f32x2 *>(kept + m * G::kKept) + lane;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) hs[0][q][i] = from[(q * NP + i) * 32];
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                b[k].read(at.bc + (r0 + k) * SP + s0);
+                c[k].read(at.bc + G::kMatrix + (r0 + k) * SP + s0);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    x[k][q] = step[q][(r0 + k) * 2];
+                    const f32x2 dt = pack2(x[k][q].x, x[k][q].x), du = pack2(x[k][q].y, x[k][q].y);
+                    f32x2 o = 0;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        a[k][q][i] = ex2_2(mul2(dt, A[q].v[i]));
+                        hs[k + 1][q][i] = fma2(a[k][q][i], hs[k][q][i], mul2(du, b[k].v[i]));
+                        o = i ? fma2(hs[k + 1][q][i], c[k].v[i], o) : mul2(hs[k + 1][q][i], c[k].v[i]);
+                    }
+                    const float2 f = unpack2(o);
+                    y[k][q] = f.x + f.y;
+                }
+            }
+            __syncwarp();  // the kept states of all lanes have been read: their place is used again
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                y[k][0] += __shfl_xor_sync(~0u, y[k][1], 1);
+                y[k][0] += __shfl_xor_sync(~0u, y[k][0], 2);
+            }
+            float *out = outs + odd * G::kOutHalf + pair * G::kOutPitch + m * Q;
+            if (j < 2) {
+#pragma unroll
+                for (int k = 0; k < Q; ++k) out[k] = y[k][0];
+            }
+            float share[Q];
+#pragma unroll
+            for (int k = Q - 1; k >= 0; --k) {
+                f32x2 vB[NP], vC[NP];
+                float s1[2], s2[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float of = dos[q][(r0 + k) * 2];
+                    const f32x2 o = pack2(of, of), du = pack2(x[k][q].y, x[k][q].y);
+                    const f32x2 dt = pack2(x[k][q].x, x[k][q].x);
+                    f32x2 gB = 0, qA = 0;
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        const f32x2 now = fma2(c[k].v[i], o, g[q].v[i]);
+                        vC[i] = q ? fma2(o, hs[k + 1][q][i], vC[i]) : mul2(o, hs[k + 1][q][i]);
+                        vB[i] = q ? fma2(du, now, vB[i]) : mul2(du, now);
+                        gB = i ? fma2(now, b[k].v[i], gB) : mul2(now, b[k].v[i]);
+                        g[q].v[i] = mul2(now, a[k][q][i]);
+                        const f32x2 w = mul2(g[q].v[i], hs[k][q][i]);
+                        qA = i ? fma2(w, A[q].v[i], qA) : mul2(w, A[q].v[i]);
+                        dA[q].v[i] = fma2(w, dt, dA[q].v[i]);
+                    }
+                    const float2 f1 = unpack2(gB), f2 = unpack2(qA);
+                    s1[q] = f1.x + f1.y;
+                    s2[q] = f2.x + f2.y;
+                }
+                // lanes 0, 1 of the pair end with g . B, lanes 2, 3 with q . A
+                s1[0] += __shfl_xor_sync(~0u, s1[1], 1);
+                s2[0] += __shfl_xor_sync(~0u, s2[1], 1);
+                share[k] = (j & 2 ? s2[0] : s1[0]) + __shfl_xor_sync(~0u, j & 2 ? s1[0] : s2[0], 2);
+                float v[2][SPT];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const float2 fB = unpack2(vB[i]), fC = unpack2(vC[i]);
+                    v[0][2 * i < SPT ? 2 * i : 0] = fB.x;
+                    v[1][2 * i < SPT ? 2 * i : 0] = fC.x;
+                    if constexpr (SPT > 1) {
+                        v[0][2 * i + 1] = fB.y;
+                        v[1][2 * i + 1] = fC.y;
+                    }
+                }
+                int state = s0, mat = 0;
+                PairSum<SPT, 2, SPT, 16>::run(v, lane, state, mat);
+                float *to = kept + m * G::kKept + k * 2 * SP + mat * SP + state;
+#pragma unroll
+                for (int w = 0; w < PairShare<SPT>::MATS; ++w)
+#pragma unroll
+                    for (int i = 0; i < PairShare<SPT>::N; ++i) to[w * SP + i] = v[w][i];
+            }
+            float *sums = outs + (1 + (j >> 1)) * G::kOut + odd * G::kOutHalf + pair * G::kOutPitch + m * Q;
+#pragma unroll
+            for (int k = 0; k < Q; ++k) sums[k] = share[k];
+        }
+        __syncwarp();
+        // the rows that the lane read: dz, du, ddelta
+        const int stop = t0 + min(p.L - t0, TT), end = min(at.len, stop);
+        const int t_lane = at.quarter * VE;
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            const int c = lane / 4, place = k * G::kOutHalf + c * G::kOutPitch + t_lane;
+            const bool on = c + 8 * k < at.c_count;
+            const int64_t row = (rows + c + 8 * k) * p.L;
+            float wz[VE], wu[VE], wd[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const bool in = on && t0 + t_lane + e < end;
+                const float uu = at.ru[k][e], raw = at.rd[k][e] + at.bias[k];
+                const float dt = reinterpret_cast<const float2 *>(
+                    at.steps)[(c * G::kStepPitch + t_lane + at.quarter + e) * 2 + k].x;
+                const float o = at.dos[(c * G::kDoPitch + t_lane + at.quarter + e) * 2 + k];
+                const float gB = outs[G::kOut + place + e], qA = outs[2 * G::kOut + place + e];
+                float ddt = fmaf(gB, uu, qA * kLn2);
+                if (p.softplus) ddt *= sigmoid(raw);
+                wd[e] = in ? ddt : 0.f;
+                wu[e] = in ? fmaf(gB, dt, D[k] * o) : 0.f;
+                dbias[k] += wd[e];
+                dD[k] = fmaf(o, uu, dD[k]);
+                if (at.z)
+                    wz[e] = in ? at.ry[k][e] * fmaf(D[k], uu, outs[place + e]) * silu_grad(at.rz[k][e])
+                               : 0.f;
+            }
+            if (on) {
+                Run<T, VE> r;
+                r.put(wu);
+                store_run(r, static_cast<T *>(p.du) + row, t0 + t_lane, stop, p.vec_y);
+                r.put(wd);
+                store_run(r, static_cast<T *>(p.ddelta) + row, t0 + t_lane, stop, p.vec_y);
+                if (at.z) {
+                    r.put(wz);
+                    store_run(r, static_cast<T *>(p.dz) + row, t0 + t_lane, stop, p.vec_y);
+                }
+            }
+        }
+        // this block's share of dB and dC: the warps' in their order
+        __syncthreads();
+        const int64_t share_rows = ((int64_t)blockIdx.x * p.N + at.n) * p.L + t0;
+        const int64_t matrix = (int64_t)gridDim.x * p.N * p.L * p.S;
+        for (int i = threadIdx.x; i < TT * 2 * SP; i += kBackThreads) {
+            const int t = i / (2 * SP), r = i % (2 * SP), s = r % SP;
+            const float *q = kept_all + t / Q * G::kKept + t % Q * (2 * SP) + r;
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kBackWarps; ++w) v += q[w * G::kKeptAll];
+            if (s < p.S && t0 + t < stop) p.part_bc[r / SP * matrix + (share_rows + t) * p.S + s] = v;
+        }
+    }
+    const int64_t part = ((int64_t)at.n * p.segments + seg) * p.channels + at.c_base;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+        if (mine[q] < at.c_count) dA[q].store(p.part_a + (part + mine[q]) * (p.S + 2), s0, p.S);
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+        dD[k] = sum4(dD[k]);
+        dbias[k] = sum4(dbias[k]);
+        const int c = lane / 4 + 8 * k;
+        if (at.quarter == 0 && c < at.c_count) {
+            p.part_a[(part + c) * (p.S + 2) + p.S] = dD[k];
+            p.part_a[(part + c) * (p.S + 2) + p.S + 1] = dbias[k];
+        }
     }
 }
 
@@ -326,29 +545,32 @@ __global__ void __launch_bounds__(256) join_bc_kernel(const ScanParams p) {
 }
 
 struct Layout {
-    int64_t h, g, dt, bc, a, total;  // float offsets
+    int64_t h, g, dt, dts, bc, a, total;  // float offsets
 };
 
-// Sizes of the backward pass for these arguments: chunks, segments and where
+// Sizes of the backward pass for these arguments: tiles, segments and where
 // the workspace's parts start.
 Layout plan(ScanParams &p) {
     const int tt = p.S <= 16 ? 32 : p.S <= 32 ? 16 : 8;
-    p.chunks = (p.L + tt - 1) / tt;
-    p.chunk_len = tt;
+    p.blocks_per_group = (p.per_group + 63) / 64;
+    p.tiles = (p.L + tt - 1) / tt;
     const int64_t blocks = (int64_t)p.groups * p.blocks_per_group;
-    // chunks of a segment: as few shares of dA as leave eight blocks per SM
-    int64_t per = blocks * p.N * p.chunks / (8 * kSMs);
+    // tiles of a segment: as many (fewer shares of dA, fewer of g's states) as
+    // leave six blocks per SM, three waves of them
+    int64_t per = blocks * p.N * p.tiles / (6 * kSMs);
     per = per < 1 ? 1 : per > 16 ? 16 : per;
-    p.chunks_per_segment = (int)per;
-    p.segments = (int)((p.chunks + per - 1) / per);
+    p.tiles_per_segment = (int)per;
+    p.segments = (int)((p.tiles + per - 1) / per);
     auto up = [](int64_t v) { return (v + 3) / 4 * 4; };
+    const int64_t rows = (int64_t)p.N * p.channels;
     Layout l;
     l.h = 0;
-    l.g = l.h + up((int64_t)p.N * p.chunks * p.channels * p.S);
-    l.dt = l.g + up((int64_t)p.N * p.chunks * p.channels * p.S);
-    l.bc = l.dt + up((int64_t)p.N * p.chunks * p.channels);
+    l.g = l.h + up(rows * p.tiles * p.S);
+    l.dt = l.g + up(rows * p.segments * p.S);
+    l.dts = l.dt + up(rows * p.tiles);
+    l.bc = l.dts + up(rows * p.segments);
     l.a = l.bc + up(2 * blocks * p.N * p.L * p.S);
-    l.total = l.a + up((int64_t)p.N * p.segments * p.channels * (p.S + 2));
+    l.total = l.a + up(rows * p.segments * (p.S + 2));
     return l;
 }
 
@@ -426,24 +648,27 @@ SPCONV_API int spconv_scan_backward(const spconv_scan_args *a, void *stream) {
     }
     const Layout l = plan(p);
     float *ws = static_cast<float *>(a->workspace);
-    p.h_chunk = ws + l.h; p.g_chunk = ws + l.g; p.dt_chunk = ws + l.dt;
+    p.h_chunk = ws + l.h; p.g_chunk = ws + l.g; p.dt_chunk = ws + l.dt; p.dt_segment = ws + l.dts;
     p.part_bc = ws + l.bc; p.part_a = ws + l.a;
     p.vec_y = rows_aligned(a->du, 0, L, e) && rows_aligned(a->ddelta, 0, L, e) &&
               (!a->dz || rows_aligned(a->dz, 0, L, e));
     const int64_t weights = (int64_t)p.channels * (p.S + 2), bc = 2LL * p.groups * p.N * L * p.S;
-    if (p.chunks > 65535 || (bc + 255) / 256 > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
+    if (p.segments > 65535 || (bc + 255) / 256 > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
     return by_dtype(a->dtype, [&](auto t) {
         return by_states(a->S, [&](auto k) {
             using T = decltype(t);
-            constexpr int SPT = decltype(k)::value, smem = gradient_smem<SPT>() * 4;
-            static_assert(smem <= 227 * 1024, "a tile fits shared memory");
-            const dim3 grid(p.groups * p.blocks_per_group, p.N, p.chunks);
-            chunk_ends_kernel<T, SPT><<<grid, kScanThreads, 0, s>>>(p);
+            constexpr int SPT = decltype(k)::value;
+            using G = BackTile<SPT>;
+            static_assert(G::kAll * 4 <= 227 * 1024, "a tile fits shared memory");
+            const dim3 grid(p.groups * p.blocks_per_group, p.N, p.segments);
+            auto *ends = segment_ends_kernel<T, SPT>;
+            auto *grad = gradient_kernel<T, SPT>;
+            if (int rc = raise_smem(reinterpret_cast<const void *>(ends), G::kEnds * 4)) return rc;
+            if (int rc = raise_smem(reinterpret_cast<const void *>(grad), G::kAll * 4)) return rc;
+            ends<<<grid, kBackThreads, G::kEnds * 4, s>>>(p);
             if (int rc = launch_status()) return rc;
             if (int rc = scan_join_chunks(p, true, s)) return rc;
-            auto *fn = gradient_kernel<T, SPT>;
-            if (int rc = raise_smem(reinterpret_cast<const void *>(fn), smem)) return rc;
-            fn<<<dim3(grid.x, grid.y, p.segments), kScanThreads, smem, s>>>(p);
+            grad<<<grid, kBackThreads, G::kAll * 4, s>>>(p);
             if (int rc = launch_status()) return rc;
             join_weights_kernel<<<(unsigned)((weights + 255) / 256), 256, 0, s>>>(p);
             join_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(p);
