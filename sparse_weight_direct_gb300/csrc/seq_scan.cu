@@ -242,31 +242,32 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanParams p) {
             }
         }
         __syncwarp();
-        if (ENDS) continue;
+        if constexpr (!ENDS) {
 #pragma unroll
-        for (int k = 0; k < NI; ++k) {
-            const int c = lane / 4 + 8 * k;
-            const float4 *q = reinterpret_cast<const float4 *>(
-                outs + c / G::PAIRS * G::kOutHalf + c % G::PAIRS * G::kOutPitch + t_mine);
-            float o[VE];
+            for (int k = 0; k < NI; ++k) {
+                const int c = lane / 4 + 8 * k;
+                const float4 *q = reinterpret_cast<const float4 *>(
+                    outs + c / G::PAIRS * G::kOutHalf + c % G::PAIRS * G::kOutPitch + t_mine);
+                float o[VE];
 #pragma unroll
-            for (int e = 0; e < VE; e += 4) {
-                const float4 f = q[e / 4];
-                const float y[4] = {f.x, f.y, f.z, f.w};
+                for (int e = 0; e < VE; e += 4) {
+                    const float4 f = q[e / 4];
+                    const float y[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[e + i] = fmaf(D[k], u[k][e + i], y[i]);
+                    for (int i = 0; i < 4; ++i) o[e + i] = fmaf(D[k], u[k][e + i], y[i]);
+                }
+                if (zb) {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) o[e] *= silu(z[k][e]);
+                }
+                if (t0 + TT > end)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) o[e] = t0 + t_mine + e < end ? o[e] : 0.f;
+                Run<T, VE> out;
+                out.put(o);
+                if (c < c_count)
+                    store_run(out, static_cast<T *>(p.y) + (rows + c) * p.L, t0 + t_mine, stop, p.vec_y);
             }
-            if (zb) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) o[e] *= silu(z[k][e]);
-            }
-            if (t0 + TT > end)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) o[e] = t0 + t_mine + e < end ? o[e] : 0.f;
-            Run<T, VE> out;
-            out.put(o);
-            if (c < c_count)
-                store_run(out, static_cast<T *>(p.y) + (rows + c) * p.L, t0 + t_mine, stop, p.vec_y);
         }
     }
     if (ENDS) {
@@ -342,44 +343,80 @@ __global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, in
     if (back && p.dstate) p.dstate[i] = v;
 }
 
-// Step: four lanes per request and channel, as in the scan; the states are
-// read and written once.
+// Step: four lanes per request and channel, each with SPT of its states, which
+// are read and written once.  Bound by that traffic.
 template <typename T, int SPT>
 __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 2;
-    const int j = threadIdx.x & 3, s0 = j * SPT;
-    const bool on = i < (int64_t)p.N * p.channels;
-    const int n = on ? (int)(i / p.channels) : 0, c = on ? (int)(i - (int64_t)n * p.channels) : 0;
+    const int64_t c64 = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
+    const int n = blockIdx.y, j = threadIdx.x & 3, s0 = j * SPT;
+    const bool on = c64 < p.channels;
+    const int c = on ? (int)c64 : 0;
     const int slot = !on ? -1 : p.slots ? p.slots[n] : n;
     const bool live = slot >= 0 && slot < p.num_slots;
+    const T *zp = static_cast<const T *>(p.z) + n * p.z_sn + c;
     float o = 0.f;
     if (live) {
-        const int g = c / p.per_group;
-        const float u = to_f32(static_cast<const T *>(p.u)[n * p.u_sn + c]);
-        const float raw = to_f32(static_cast<const T *>(p.delta)[n * p.d_sn + c]) +
-                          (p.delta_bias ? p.delta_bias[c] : 0.f);
-        const float dt = step_size(p, raw);
+        const int g = p.groups > 1 ? c / p.per_group : 0;
         const T *B = static_cast<const T *>(p.B) + n * p.b_sn + g * p.b_sg;
         const T *C = static_cast<const T *>(p.C) + n * p.c_sn + g * p.c_sg;
         float *row = p.pool + ((int64_t)slot * p.channels + c) * p.S;
-        float A[SPT], h[SPT];
-        load_states<SPT>(h, row, s0, p.S);
-        load_states<SPT>(A, p.A + (int64_t)c * p.S, s0, p.S);
+        const float *rowA = p.A + (int64_t)c * p.S;
+        float A[SPT], h[SPT], b[SPT], cc[SPT];
+        bool whole = false;
+        if constexpr (SPT % 4 == 0) {
+            whole = p.vec && p.S == 4 * SPT;
+            if (whole) {
+#pragma unroll
+                for (int k = 0; k < SPT; k += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(row + s0 + k);
+                    const float4 e = *reinterpret_cast<const float4 *>(rowA + s0 + k);
+                    h[k] = f.x; h[k + 1] = f.y; h[k + 2] = f.z; h[k + 3] = f.w;
+                    A[k] = e.x; A[k + 1] = e.y; A[k + 2] = e.z; A[k + 3] = e.w;
+                    Run<T, 4> rb, rc;
+                    load_run(rb, B, s0 + k, p.S, true);
+                    load_run(rc, C, s0 + k, p.S, true);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        b[k + i] = rb[i];
+                        cc[k + i] = rc[i];
+                    }
+                }
+            }
+        }
+        if (!whole) {
+            load_states<SPT>(h, row, s0, p.S);
+            load_states<SPT>(A, rowA, s0, p.S);
+#pragma unroll
+            for (int k = 0; k < SPT; ++k) {
+                b[k] = s0 + k < p.S ? to_f32(B[s0 + k]) : 0.f;
+                cc[k] = s0 + k < p.S ? to_f32(C[s0 + k]) : 0.f;
+            }
+        }
+        const float u = to_f32(static_cast<const T *>(p.u)[n * p.u_sn + c]);
+        const float raw = to_f32(static_cast<const T *>(p.delta)[n * p.d_sn + c]) +
+                          (p.delta_bias ? p.delta_bias[c] : 0.f);
+        const float dt = p.softplus ? softplus(raw) : raw;
 #pragma unroll
         for (int k = 0; k < SPT; ++k) {
-            const bool in = s0 + k < p.S;
-            const float b = in ? to_f32(B[s0 + k]) : 0.f, cc = in ? to_f32(C[s0 + k]) : 0.f;
-            h[k] = fmaf(ex2(dt * (A[k] * kLog2e)), h[k], dt * u * b);
-            o = fmaf(h[k], cc, o);
+            h[k] = fmaf(ex2(dt * (A[k] * kLog2e)), h[k], dt * u * b[k]);
+            o = fmaf(h[k], cc[k], o);
         }
-        store_states<SPT>(row, h, s0, p.S);
+        if constexpr (SPT % 4 == 0) {
+            if (whole) {
+#pragma unroll
+                for (int k = 0; k < SPT; k += 4)
+                    *reinterpret_cast<float4 *>(row + s0 + k) =
+                        make_float4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+            }
+        }
+        if (!whole) store_states<SPT>(row, h, s0, p.S);
         if (j == 0 && p.D) o = fmaf(p.D[c], u, o);
     }
     o += __shfl_xor_sync(~0u, o, 1);
     o += __shfl_xor_sync(~0u, o, 2);
     if (on && j == 0) {
-        if (p.z && live) o *= silu(to_f32(static_cast<const T *>(p.z)[n * p.z_sn + c]));
-        static_cast<T *>(p.y)[i] = from_f32<T>(o);
+        if (p.z && live) o *= silu(to_f32(*zp));
+        static_cast<T *>(p.y)[(int64_t)n * p.channels + c] = from_f32<T>(o);
     }
 }
 
@@ -559,6 +596,7 @@ SPCONV_API int spconv_scan(const spconv_scan_args *a, void *stream) {
 SPCONV_API int spconv_scan_step(const spconv_scan_args *a, void *stream) {
     const int st = scan_check_sizes(a);
     if (st) return st;
+    if (a->N > 65535) return SPCONV_ERR_UNSUPPORTED;  // requests go along grid y
     if (a->num_slots < 0 || (!a->slots && a->num_slots != a->N) || a->u_stride_c != 1 ||
         a->delta_stride_c != 1 || (a->z && a->z_stride_c != 1) || a->b_stride_s != 1 ||
         a->c_stride_s != 1)
@@ -580,13 +618,15 @@ SPCONV_API int spconv_scan_step(const spconv_scan_args *a, void *stream) {
             overlap(o.first, o.second, a->C, extent(a->N, a->groups, a->S, a->c_stride_n, a->c_stride_g, e)))
             return SPCONV_ERR_INVALID_ARG;
     if (overlap(a->y, yb, a->pool, sb)) return SPCONV_ERR_INVALID_ARG;
-    const ScanParams p = scan_params(a);
-    const int64_t blocks = (rows * 4 + 255) / 256;
-    if (blocks > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
+    ScanParams p = scan_params(a);
+    p.vec = aligned(a->pool, 16) && aligned(a->A, 16) &&
+            rows_aligned(a->B, a->b_stride_n, a->b_stride_g, e) &&
+            rows_aligned(a->C, a->c_stride_n, a->c_stride_g, e);
+    const dim3 grid((unsigned)((a->channels + 63) / 64), a->N);  // 64 channels of a block
     return by_dtype(a->dtype, [&](auto t) {
         return by_states(a->S, [&](auto k) {
             scan_step_kernel<decltype(t), decltype(k)::value>
-                <<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+                <<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
             return launch_status();
         });
     });

@@ -31,11 +31,6 @@ struct ScanParams {
     int vec_y;                     // output rows (N x channels x L) likewise
 };
 
-// The step size of one position.
-static __device__ __forceinline__ float step_size(const ScanParams &p, float raw) {
-    return p.softplus ? softplus(raw) : raw;
-}
-
 // The lane's SPT states as pairs; one state (S <= 4) leaves the second half
 // of its pair at zero.
 template <int SPT>

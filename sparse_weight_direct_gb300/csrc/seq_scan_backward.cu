@@ -555,12 +555,18 @@ Layout plan(ScanParams &p) {
     p.blocks_per_group = (p.per_group + 63) / 64;
     p.tiles = (p.L + tt - 1) / tt;
     const int64_t blocks = (int64_t)p.groups * p.blocks_per_group;
-    // tiles of a segment: as many (fewer shares of dA, fewer of g's states) as
-    // leave six blocks per SM, three waves of them
-    int64_t per = blocks * p.N * p.tiles / (6 * kSMs);
-    per = per < 1 ? 1 : per > 16 ? 16 : per;
-    p.tiles_per_segment = (int)per;
-    p.segments = (int)((p.tiles + per - 1) / per);
+    // tiles of a segment: two blocks fit an SM, and the blocks run in waves, so
+    // the time goes by waves x tiles; of equals the longest (it has the fewest shares
+    // of dA and the fewest of g's states)
+    int64_t best = 0;
+    for (int per = 1; per <= 8 && per <= p.tiles; ++per) {
+        const int64_t segments = (p.tiles + per - 1) / per;
+        const int64_t waves = (blocks * p.N * segments + 2 * kSMs - 1) / (2 * kSMs);
+        if (best && waves * per > best) continue;
+        best = waves * per;
+        p.tiles_per_segment = per;
+        p.segments = (int)segments;
+    }
     auto up = [](int64_t v) { return (v + 3) / 4 * 4; };
     const int64_t rows = (int64_t)p.N * p.channels;
     Layout l;
