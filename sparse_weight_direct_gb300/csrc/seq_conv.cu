@@ -77,11 +77,11 @@ static __device__ __forceinline__ void load_behind(float *s, const T *row, int t
     }
 }
 
-// Forward: a thread computes kVec consecutive outputs of one row; blocks x go
+// Forward: a thread computes kVec consecutive outputs of one channel in one
+// sequence after the other, the next one's inputs on their way; blocks x go
 // over the tiles of a row and the channels, y over the sequences.  Its
-// instructions are as near a bound as its bytes: 64-bit divisions for a
-// thread's place and single loads of the K-1 inputs to the left took 43 an
-// output and 94 us on 8 x 4096 x 2048 in bf16.
+// instructions are as near a bound as its bytes: a thread per run spent two
+// thirds of them on its place and its weights (82 us on 8 x 4096 x 2048 in bf16).
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p) {
     const unsigned cb = blockIdx.x / (unsigned)p.tiles;
@@ -94,21 +94,41 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p) {
 #pragma unroll
     for (int k = 0; k < K; ++k) w[k] = p.weight[(int64_t)c * K + k];
     const float b = p.bias ? p.bias[c] : 0.f;
+    const int64_t x_step = gridDim.y * p.x_sn, row_step = (int64_t)gridDim.y * p.C;
+    const T *x = static_cast<const T *>(p.x) + blockIdx.y * p.x_sn + c * p.x_sc;
+    int64_t row = (int64_t)blockIdx.y * p.C + c;
+    struct Inputs {
+        Run<T> in;
+        float left[K > 1 ? K - 1 : 1];
+        int len;
+    } next;
+    auto fetch = [&](int n) {
+        if (n >= p.N) return;
+        next.len = length_of(p.lengths, n, p.L);
+        if (t0 < next.len) {
+            load_run(next.in, x, t0, next.len, p.vec_x);
+            load_before<T, K>(next.left, x,
+                              p.state ? static_cast<const T *>(p.state) + row * (K - 1) : nullptr,
+                              t0, next.len, p.vec_x);
+        }
+    };
+    fetch(blockIdx.y);
     for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
-        const int len = length_of(p.lengths, n, p.L);
-        const int64_t rowi = (int64_t)n * p.C + c;
-        const T *row = static_cast<const T *>(p.x) + n * p.x_sn + c * p.x_sc;
-        const T *st = p.state ? static_cast<const T *>(p.state) + rowi * (K - 1) : nullptr;
+        const Inputs now = next;
+        const T *xrow = x;
+        const int64_t rowi = row;
+        x += x_step;
+        row += row_step;
+        fetch(n + gridDim.y);
         if (run < p.runs) {
             Run<T> out;
             out.clear();
-            if (t0 < len) {
-                Run<T> in;
-                load_run(in, row, t0, len, p.vec_x);
+            if (t0 < now.len) {
                 float s[kVec + K - 1], o[kVec];
-                load_before<T, K>(s, row, st, t0, len, p.vec_x);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) s[K - 1 + i] = in[i];
+                for (int i = 0; i < K - 1; ++i) s[i] = now.left[i];
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) s[K - 1 + i] = now.in[i];
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
                     o[i] = b;
@@ -119,20 +139,21 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p) {
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) o[i] = silu(o[i]);
                 }
-                if (t0 + kVec > len) {
+                if (t0 + kVec > now.len) {
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) o[i] = t0 + i < len ? o[i] : 0.f;
+                    for (int i = 0; i < kVec; ++i) o[i] = t0 + i < now.len ? o[i] : 0.f;
                 }
                 out.put(o);
             }
             store_run(out, static_cast<T *>(p.y) + rowi * p.L, t0, p.L, p.vec_y);
         }
         if (K > 1 && p.final_state && run == 0) {
+            const T *st = p.state ? static_cast<const T *>(p.state) + rowi * (K - 1) : nullptr;
             T *fin = static_cast<T *>(p.final_state) + rowi * (K - 1);
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
-                const int t = len - (K - 1) + j;
-                fin[j] = t >= 0 ? row[t] : st ? st[t + K - 1] : from_f32<T>(0.f);
+                const int t = now.len - (K - 1) + j;
+                fin[j] = t >= 0 ? xrow[t] : st ? st[t + K - 1] : from_f32<T>(0.f);
             }
         }
     }
@@ -411,7 +432,11 @@ SPCONV_API int spconv_short_conv(const spconv_short_conv_args *a, void *stream) 
     p.tiles = (runs + p.tx - 1) / p.tx;
     const int64_t blocks = ((int64_t)a->C + p.ty - 1) / p.ty * p.tiles;
     if (blocks > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks, a->N < 65535 ? a->N : 65535);
+    // sequences side by side as far as 16 blocks per SM need them
+    int64_t side = (16 * kSMs + blocks - 1) / blocks;
+    if (side > a->N) side = a->N;
+    if (side > 65535) side = 65535;
+    const dim3 grid((unsigned)blocks, (unsigned)side);
     return by_dtype(a->dtype, [&](auto t) {
         return by_taps(a->K, [&](auto k) {
             conv_kernel<decltype(t), decltype(k)::value>

@@ -344,79 +344,96 @@ __global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, in
 }
 
 // Step: four lanes per request and channel, each with SPT of its states, which
-// are read and written once.  Bound by that traffic.
+// are read and written once.  Bound by that traffic, so by how much of it is
+// under way: a thread takes one request after the other for its channel, with
+// the next one's states and inputs being read, and its row of A once.  (One
+// request per thread, 128 x 4096 x 16 in bf16: 28 us.)
 template <typename T, int SPT>
 __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
     const int64_t c64 = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
-    const int n = blockIdx.y, j = threadIdx.x & 3, s0 = j * SPT;
+    const int j = threadIdx.x & 3, s0 = j * SPT;
     const bool on = c64 < p.channels;
-    const int c = on ? (int)c64 : 0;
-    const int slot = !on ? -1 : p.slots ? p.slots[n] : n;
-    const bool live = slot >= 0 && slot < p.num_slots;
-    const T *zp = static_cast<const T *>(p.z) + n * p.z_sn + c;
-    float o = 0.f;
-    if (live) {
-        const int g = p.groups > 1 ? c / p.per_group : 0;
-        const T *B = static_cast<const T *>(p.B) + n * p.b_sn + g * p.b_sg;
-        const T *C = static_cast<const T *>(p.C) + n * p.c_sn + g * p.c_sg;
-        float *row = p.pool + ((int64_t)slot * p.channels + c) * p.S;
-        const float *rowA = p.A + (int64_t)c * p.S;
-        float A[SPT], h[SPT], b[SPT], cc[SPT];
-        bool whole = false;
+    const int c = on ? (int)c64 : 0, g = p.groups > 1 ? c / p.per_group : 0;
+    const bool whole = SPT % 4 == 0 && p.vec && p.S == 4 * SPT;
+    const T *u = static_cast<const T *>(p.u) + c, *d = static_cast<const T *>(p.delta) + c;
+    const T *z = static_cast<const T *>(p.z) + c;
+    const T *B = static_cast<const T *>(p.B) + g * p.b_sg, *C = static_cast<const T *>(p.C) + g * p.c_sg;
+    const float bias = p.delta_bias ? p.delta_bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
+    float A[SPT];
+    load_states<SPT>(A, p.A + (int64_t)c * p.S, s0, p.S);
+#pragma unroll
+    for (int k = 0; k < SPT; ++k) A[k] *= kLog2e;
+    struct Inputs {
+        float *row;  // the request's states, nullptr without
+        float h[SPT], b[SPT], c[SPT], u, d, z;
+    } next;
+    auto fetch = [&](int n) {
+        next.row = nullptr;
+        if (n >= p.N || !on) return;
+        const int slot = p.slots ? p.slots[n] : n;
+        if (slot < 0 || slot >= p.num_slots) return;
+        next.row = p.pool + ((int64_t)slot * p.channels + c) * p.S;
+        next.u = to_f32(u[n * p.u_sn]);
+        next.d = to_f32(d[n * p.d_sn]);
+        if (p.z) next.z = to_f32(z[n * p.z_sn]);
+        const T *Bn = B + n * p.b_sn, *Cn = C + n * p.c_sn;
         if constexpr (SPT % 4 == 0) {
-            whole = p.vec && p.S == 4 * SPT;
             if (whole) {
 #pragma unroll
                 for (int k = 0; k < SPT; k += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(row + s0 + k);
-                    const float4 e = *reinterpret_cast<const float4 *>(rowA + s0 + k);
-                    h[k] = f.x; h[k + 1] = f.y; h[k + 2] = f.z; h[k + 3] = f.w;
-                    A[k] = e.x; A[k + 1] = e.y; A[k + 2] = e.z; A[k + 3] = e.w;
+                    const float4 f = *reinterpret_cast<const float4 *>(next.row + s0 + k);
+                    next.h[k] = f.x; next.h[k + 1] = f.y; next.h[k + 2] = f.z; next.h[k + 3] = f.w;
                     Run<T, 4> rb, rc;
-                    load_run(rb, B, s0 + k, p.S, true);
-                    load_run(rc, C, s0 + k, p.S, true);
+                    load_run(rb, Bn, s0 + k, p.S, true);
+                    load_run(rc, Cn, s0 + k, p.S, true);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        b[k + i] = rb[i];
-                        cc[k + i] = rc[i];
+                        next.b[k + i] = rb[i];
+                        next.c[k + i] = rc[i];
                     }
                 }
+                return;
             }
         }
-        if (!whole) {
-            load_states<SPT>(h, row, s0, p.S);
-            load_states<SPT>(A, rowA, s0, p.S);
-#pragma unroll
-            for (int k = 0; k < SPT; ++k) {
-                b[k] = s0 + k < p.S ? to_f32(B[s0 + k]) : 0.f;
-                cc[k] = s0 + k < p.S ? to_f32(C[s0 + k]) : 0.f;
-            }
-        }
-        const float u = to_f32(static_cast<const T *>(p.u)[n * p.u_sn + c]);
-        const float raw = to_f32(static_cast<const T *>(p.delta)[n * p.d_sn + c]) +
-                          (p.delta_bias ? p.delta_bias[c] : 0.f);
-        const float dt = p.softplus ? softplus(raw) : raw;
+        load_states<SPT>(next.h, next.row, s0, p.S);
 #pragma unroll
         for (int k = 0; k < SPT; ++k) {
-            h[k] = fmaf(ex2(dt * (A[k] * kLog2e)), h[k], dt * u * b[k]);
-            o = fmaf(h[k], cc[k], o);
+            next.b[k] = s0 + k < p.S ? to_f32(Bn[s0 + k]) : 0.f;
+            next.c[k] = s0 + k < p.S ? to_f32(Cn[s0 + k]) : 0.f;
         }
-        if constexpr (SPT % 4 == 0) {
-            if (whole) {
+    };
+    fetch(blockIdx.y);
+    for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
+        Inputs now = next;
+        fetch(n + gridDim.y);
+        float o = 0.f;
+        if (now.row) {
+            const float raw = now.d + bias, dt = p.softplus ? softplus(raw) : raw;
+            const float du = dt * now.u;
 #pragma unroll
-                for (int k = 0; k < SPT; k += 4)
-                    *reinterpret_cast<float4 *>(row + s0 + k) =
-                        make_float4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+            for (int k = 0; k < SPT; ++k) {
+                now.h[k] = fmaf(ex2(dt * A[k]), now.h[k], du * now.b[k]);
+                o = fmaf(now.h[k], now.c[k], o);
             }
+            if constexpr (SPT % 4 == 0) {
+                if (whole) {
+#pragma unroll
+                    for (int k = 0; k < SPT; k += 4)
+                        *reinterpret_cast<float4 *>(now.row + s0 + k) =
+                            make_float4(now.h[k], now.h[k + 1], now.h[k + 2], now.h[k + 3]);
+                }
+            }
+            if (!whole) store_states<SPT>(now.row, now.h, s0, p.S);
         }
-        if (!whole) store_states<SPT>(row, h, s0, p.S);
-        if (j == 0 && p.D) o = fmaf(p.D[c], u, o);
-    }
-    o += __shfl_xor_sync(~0u, o, 1);
-    o += __shfl_xor_sync(~0u, o, 2);
-    if (on && j == 0) {
-        if (p.z && live) o *= silu(to_f32(*zp));
-        static_cast<T *>(p.y)[(int64_t)n * p.channels + c] = from_f32<T>(o);
+        o += __shfl_xor_sync(~0u, o, 1);
+        o += __shfl_xor_sync(~0u, o, 2);
+        if (on && j == 0) {
+            if (now.row) {
+                o = fmaf(D, now.u, o);
+                if (p.z) o *= silu(now.z);
+            }
+            static_cast<T *>(p.y)[(int64_t)n * p.channels + c] = from_f32<T>(o);
+        }
     }
 }
 
@@ -622,7 +639,10 @@ SPCONV_API int spconv_scan_step(const spconv_scan_args *a, void *stream) {
     p.vec = aligned(a->pool, 16) && aligned(a->A, 16) &&
             rows_aligned(a->B, a->b_stride_n, a->b_stride_g, e) &&
             rows_aligned(a->C, a->c_stride_n, a->c_stride_g, e);
-    const dim3 grid((unsigned)((a->channels + 63) / 64), a->N);  // 64 channels of a block
+    const int64_t blocks = ((int64_t)a->channels + 63) / 64;  // 64 channels of a block
+    int64_t side = (8 * kSMs + blocks - 1) / blocks;  // requests side by side: 8 blocks per SM
+    if (side > a->N) side = a->N;
+    const dim3 grid((unsigned)blocks, (unsigned)side);
     return by_dtype(a->dtype, [&](auto t) {
         return by_states(a->S, [&](auto k) {
             scan_step_kernel<decltype(t), decltype(k)::value>

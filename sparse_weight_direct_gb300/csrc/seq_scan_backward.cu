@@ -163,7 +163,7 @@ struct BackPlace {
 template <typename T, int SPT>
 __global__ void __launch_bounds__(kBackThreads) segment_ends_kernel(const ScanParams p) {
     using G = BackTile<SPT>;
-    constexpr int VE = G::VE, TT = G::TT, SP = G::SP, NP = G::NP, NI = G::NI;
+    constexpr int TT = G::TT, SP = G::SP, NP = G::NP, NI = G::NI;
     extern __shared__ __align__(16) float sm[];
     BackPlace<T, SPT> at(p, sm);
     const int pair = at.lane >> 2, j = at.lane & 3, s0 = j * SPT, seg = blockIdx.z;
