@@ -343,24 +343,29 @@ __global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, in
     if (back && p.dstate) p.dstate[i] = v;
 }
 
-// Step: four lanes per request and channel, each with SPT of its states, which
+// Step: LPC lanes per request and channel, each with SPT of its states, which
 // are read and written once.  Bound by that traffic, so by how much of it is
 // under way: a thread takes one request after the other for its channel, with
 // the next one's states and inputs being read, and its row of A once.  (One
 // request per thread, 128 x 4096 x 16 in bf16: 28 us.)
-template <typename T, int SPT>
+template <typename T, int SPT, int LPC>
 __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
-    const int64_t c64 = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2);
-    const int j = threadIdx.x & 3, s0 = j * SPT;
+    const int64_t c64 = (int64_t)blockIdx.x * (256 / LPC) + threadIdx.x / LPC;
+    // lane j holds states s0 .. s0 + SPT-1; of whole rows, fours of them LPC
+    // fours apart, so that a warp's reads and writes are contiguous
+    const int j = threadIdx.x % LPC, s0 = j * SPT;
     const bool on = c64 < p.channels;
     const int c = on ? (int)c64 : 0, g = p.groups > 1 ? c / p.per_group : 0;
-    const bool whole = SPT % 4 == 0 && p.vec && p.S == 4 * SPT;
+    const bool whole = SPT % 4 == 0 && p.vec && p.S == LPC * SPT;
     const T *u = static_cast<const T *>(p.u) + c, *d = static_cast<const T *>(p.delta) + c;
     const T *z = static_cast<const T *>(p.z) + c;
     const T *B = static_cast<const T *>(p.B) + g * p.b_sg, *C = static_cast<const T *>(p.C) + g * p.c_sg;
     const float bias = p.delta_bias ? p.delta_bias[c] : 0.f, D = p.D ? p.D[c] : 0.f;
     float A[SPT];
-    load_states<SPT>(A, p.A + (int64_t)c * p.S, s0, p.S);
+    const float *rowA = p.A + (int64_t)c * p.S;
+    auto place = [&](int k) { return whole ? (k / 4 * LPC + j) * 4 + k % 4 : s0 + k; };
+#pragma unroll
+    for (int k = 0; k < SPT; ++k) A[k] = place(k) < p.S ? rowA[place(k)] : 0.f;
 #pragma unroll
     for (int k = 0; k < SPT; ++k) A[k] *= kLog2e;
     struct Inputs {
@@ -381,11 +386,11 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
             if (whole) {
 #pragma unroll
                 for (int k = 0; k < SPT; k += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(next.row + s0 + k);
+                    const float4 f = *reinterpret_cast<const float4 *>(next.row + place(k));
                     next.h[k] = f.x; next.h[k + 1] = f.y; next.h[k + 2] = f.z; next.h[k + 3] = f.w;
                     Run<T, 4> rb, rc;
-                    load_run(rb, Bn, s0 + k, p.S, true);
-                    load_run(rc, Cn, s0 + k, p.S, true);
+                    load_run(rb, Bn, place(k), p.S, true);
+                    load_run(rc, Cn, place(k), p.S, true);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         next.b[k + i] = rb[i];
@@ -419,14 +424,14 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
                 if (whole) {
 #pragma unroll
                     for (int k = 0; k < SPT; k += 4)
-                        *reinterpret_cast<float4 *>(now.row + s0 + k) =
+                        *reinterpret_cast<float4 *>(now.row + place(k)) =
                             make_float4(now.h[k], now.h[k + 1], now.h[k + 2], now.h[k + 3]);
                 }
             }
             if (!whole) store_states<SPT>(now.row, now.h, s0, p.S);
         }
         o += __shfl_xor_sync(~0u, o, 1);
-        o += __shfl_xor_sync(~0u, o, 2);
+        if (LPC == 4) o += __shfl_xor_sync(~0u, o, 2);
         if (on && j == 0) {
             if (now.row) {
                 o = fmaf(D, now.u, o);
@@ -639,14 +644,15 @@ SPCONV_API int spconv_scan_step(const spconv_scan_args *a, void *stream) {
     p.vec = aligned(a->pool, 16) && aligned(a->A, 16) &&
             rows_aligned(a->B, a->b_stride_n, a->b_stride_g, e) &&
             rows_aligned(a->C, a->c_stride_n, a->c_stride_g, e);
-    const int64_t blocks = ((int64_t)a->channels + 63) / 64;  // 64 channels of a block
-    int64_t side = (8 * kSMs + blocks - 1) / blocks;  // requests side by side: 8 blocks per SM
-    if (side > a->N) side = a->N;
-    const dim3 grid((unsigned)blocks, (unsigned)side);
     return by_dtype(a->dtype, [&](auto t) {
-        return by_states(a->S, [&](auto k) {
-            scan_step_kernel<decltype(t), decltype(k)::value>
-                <<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        return by_tile(a->S, true, [&](auto spt, auto lpc) {
+            constexpr int SPT = decltype(spt)::value, LPC = decltype(lpc)::value, CB = 256 / LPC;
+            const int64_t blocks = ((int64_t)a->channels + CB - 1) / CB;
+            int64_t side = (4 * kSMs + blocks - 1) / blocks;  // requests side by side: 4 blocks per SM
+            if (side > a->N) side = a->N;
+            scan_step_kernel<decltype(t), SPT, LPC>
+                <<<dim3((unsigned)blocks, (unsigned)side), 256, 0,
+                   static_cast<cudaStream_t>(stream)>>>(p);
             return launch_status();
         });
     });
