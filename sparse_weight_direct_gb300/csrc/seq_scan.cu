@@ -15,259 +15,337 @@ namespace spconv {
 namespace seq {
 namespace {
 
-// Tiling.  A lane holds SPT states of each of two channels, LPC lanes hold a
+// Tiling.  A lane holds SPT states of each of four channels, four lanes hold a
 // channel, so a position's 2 * SPT values of B and C, read from shared memory,
-// serve two channels, and its step sizes, two per channel, SPT states.  A
-// broadcast read costs a 4-byte word per lane like any other, and a lane's
-// 2 * (2 * SPT) + 4 words per 2 * SPT updates are what shared memory can deliver
-// about as fast as the exponentials (32 a clock on an SM) can use them: one channel
-// and four states per lane read 2.5 words per update and took 375 us on 4 x
-// 4096 channels x 2048 positions x 16 states in bf16.
-// A block is one warp: its 64 / LPC channels give as many blocks as there are.
-template <typename T, int SPT_, int LPC_>
+// serve four channels.  (A broadcast read costs a 4-byte word per lane like any
+// other: with one and two channels per lane the reads were what bounded the
+// kernel, at 19 words a lane and position for 16 channels of 16 states.)
+// What is left to hide is latency: a sequence of 4096 channels has 128 such
+// warps, fewer than there are schedulers.  So a block has one warp for the
+// states and two that turn the next tiles' rows into step sizes and the last
+// ones' sums into outputs; tiles go through two buffers, each handed over and
+// back by a named barrier.
+template <typename T, int SPT_>
 struct ScanTile {
-    static constexpr int SPT = SPT_, LPC = LPC_, SP = SPT * LPC;
+    static constexpr int SPT = SPT_, SP = 4 * SPT;
     static constexpr int VE = 16 / sizeof(T), TT = 4 * VE;  // positions of a lane's load, of a tile
-    static constexpr int PAIRS = 32 / LPC, CW = 2 * PAIRS;  // pairs of channels, channels
-    static constexpr int NI = CW * 4 / 32;                  // loads of a lane from each row set
-    static constexpr int NB = 2 * SP * 4 / 32;              // from B and C
-    // in rows of 16 bytes {dt, dt u} of a pair's channels: one more after every
-    // VE positions, and 2 modulo 8, so that neither the lanes that write nor the
-    // pairs that read meet in the same banks
-    static constexpr int kStepPitch = TT + 10;
+    static constexpr int CB = 32;                           // channels of a block
+    static constexpr int NI = 2;                            // loads of a lane from each row set
+    static constexpr int NB = (2 * SP * 4 + 63) / 64;       // from B and C
+    // rows of a position: one more after every VE positions, and three more that
+    // are read ahead
+    static constexpr int kRows = TT + 7;
+    // {dt, dt u} of a quad's four channels: rows of 40 bytes, quads 32 modulo
+    // 128 bytes apart, so that neither the lanes that write a channel's positions
+    // nor the quads that read a position meet in a bank
+    static constexpr int kStepPitch = (5 * kRows + 11) / 16 * 16 + 4;  // of 8 bytes
     static constexpr int kOutPitch = TT + 4;
-    static constexpr int kOutHalf = PAIRS * kOutPitch + 16;  // from the pairs' first channels to
-                                                             // their second
-    static constexpr int kSteps = PAIRS * kStepPitch * 4;    // floats
-    // rows of B and of C: one more after every VE positions here too, and two
-    // that are read ahead
-    static constexpr int kMatrix = (TT + 6) * SP;
-    static constexpr int kBC = 2 * kMatrix;
-    static constexpr int kOut = 2 * kOutHalf;
+    static constexpr int kOutPart = 8 * kOutPitch + 8;  // to the quads' next channels
+    static constexpr int kSteps = 8 * kStepPitch * 2;   // floats
+    static constexpr int kOut = 4 * kOutPart;
+    static constexpr int kMatrix = kRows * SP;          // of B, of C
+    static constexpr int kBuffer = 2 * kMatrix + kSteps + kOut;
     static constexpr bool kAhead = NB <= 4;  // B and C of the next tile wait in registers
+    // decays and inputs of the next position wait in registers
+    static constexpr bool kForm = SPT <= 8;
 };
+constexpr int kScanThreads = 96;
+
+// Barriers between the two kinds of warps, one for each buffer and direction.
+// (Their numbers are constants of the instructions, or a block would take all
+// sixteen.)
+template <int ID>
+static __device__ __forceinline__ void barrier_sync() {
+    asm volatile("barrier.cta.sync %0, %1;" ::"n"(ID), "n"(kScanThreads) : "memory");
+}
+template <int ID>
+static __device__ __forceinline__ void barrier_arrive() {
+    __threadfence_block();
+    asm volatile("barrier.cta.arrive %0, %1;" ::"n"(ID), "n"(kScanThreads) : "memory");
+}
+constexpr int kFull = 1, kEmpty = 3;  // + buffer
 
 // One pass over a chunk of positions with the states in registers.
 // ENDS: from zero states, only what the chunk leaves and the sum of its step
 // sizes.  Otherwise the outputs.
-template <typename T, int SPT, int LPC, bool ENDS>
-__global__ void __launch_bounds__(32) scan_kernel(const ScanParams p) {
-    using G = ScanTile<T, SPT, LPC>;
+template <typename T, int SPT, bool ENDS>
+__global__ void __launch_bounds__(kScanThreads, SPT <= 4 ? 4 : 2) scan_kernel(const ScanParams p) {
+    using G = ScanTile<T, SPT>;
     constexpr int VE = G::VE, TT = G::TT, SP = G::SP, NP = Pairs<SPT>::N, NI = G::NI, NB = G::NB;
-    __shared__ __align__(16) float steps[G::kSteps];
-    __shared__ __align__(16) float bc[G::kBC];       // [B, C][row of TT + 6][SP]
-    __shared__ __align__(16) float outs[ENDS ? 4 : G::kOut];
-    const int lane = threadIdx.x;
-    // as owner of states: pair of channels, lane of the pair
-    const int pair = lane / LPC, j = lane % LPC, s0 = j * SPT;
-    // as owner of positions: VE * quarter .. of channels lane / 4 + 8 k
-    const int quarter = lane & 3, t_mine = quarter * VE;
-
+    extern __shared__ __align__(16) float sm[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = blockIdx.y, chunk = blockIdx.z;
     const int g = blockIdx.x / p.blocks_per_group;
-    const int c_first = (blockIdx.x - g * p.blocks_per_group) * G::CW;  // within the group
-    const int c_count = min(G::CW, p.per_group - c_first);
+    const int c_first = (blockIdx.x - g * p.blocks_per_group) * G::CB;  // within the group
+    const int c_count = min(G::CB, p.per_group - c_first);
     const int64_t c_base = (int64_t)g * p.per_group + c_first;
     const int len = p.lengths ? min(max(p.lengths[n], 0), p.L) : p.L;
     const int first = chunk * p.chunk_len, stop = first + min(p.L - first, p.chunk_len);
     const int end = max(min(len, stop), first);
+    const int tiles = (end - first + TT - 1) / TT;
     const int64_t rows = (int64_t)n * p.channels + c_base;
     const int64_t chunk_rows = ((int64_t)n * p.chunks + chunk) * p.channels + c_base;
-    const T *ub = static_cast<const T *>(p.u) + n * p.u_sn + c_base * p.u_sc;
-    const T *db = static_cast<const T *>(p.delta) + n * p.d_sn + c_base * p.d_sc;
-    const T *zb = !ENDS && p.z ? static_cast<const T *>(p.z) + n * p.z_sn + c_base * p.z_sc
+
+    if (warp == 0) {  // the states
+        const int quad = lane >> 2, j = lane & 3, s0 = j * SPT;
+        // Lane j holds the quad's channels in the order 0 ^ j, 1 ^ j, 2 ^ j, 3 ^ j: in
+        // the sums over two lanes each keeps its even ones, then its first, and
+        // gives the others, and ends with channel j.
+        int mine[4];
+        Pairs<SPT> A[4], h[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            mine[q] = quad + 8 * (q ^ j);
+            const int S = mine[q] < c_count ? p.S : 0;
+            A[q].load(p.A + (c_base + mine[q]) * p.S, s0, S);
+            A[q].scale(kLog2e);
+            if (ENDS)
+                h[q].fill(0.f);
+            else if (p.chunks > 1)
+                h[q].load(p.h_chunk + (chunk_rows + mine[q]) * p.S, s0, S);
+            else if (p.state)
+                h[q].load(p.state + (rows + mine[q]) * p.S, s0, S);
+            else
+                h[q].fill(0.f);
+        }
+        for (int i = 0; i < tiles; ++i) {
+            float *buffer = sm + (i & 1) * G::kBuffer;
+            const float *bc = buffer;
+            const float2 *step = reinterpret_cast<const float2 *>(buffer + 2 * G::kMatrix) +
+                                 quad * G::kStepPitch;
+            float *out = buffer + 2 * G::kMatrix + G::kSteps + j * G::kOutPart + quad * G::kOutPitch;
+            if (i & 1)
+                barrier_sync<kFull + 1>();
+            else
+                barrier_sync<kFull>();
+            // Two positions ahead of the states, what a position needs is read; one
+            // ahead, its decays and inputs are formed.  (Behind the tile's last
+            // position lie rows that are read and not used.)
+            float2 x[4];
+            Pairs<SPT> bn, cn, c1;
+            constexpr int NF = G::kForm ? NP : 1;
+            f32x2 a1[4][NF], b1[4][NF];
+            auto read = [&](int r) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[q] = step[r * 5 + (q ^ j)];
+                bn.read(bc + r * SP + s0);
+                if (!ENDS) cn.read(bc + G::kMatrix + r * SP + s0);
+            };
+            auto form = [&]() {
+                if constexpr (G::kForm) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x2 dt = pack2(x[q].x, x[q].x), du = pack2(x[q].y, x[q].y);
+#pragma unroll
+                        for (int k = 0; k < NP; ++k) {
+                            a1[q][k] = ex2_2(mul2(dt, A[q].v[k]));
+                            b1[q][k] = mul2(du, bn.v[k]);
+                        }
+                    }
+                    c1 = cn;
+                }
+            };
+            read(0);
+            if (G::kForm) {
+                form();
+                read(1);
+            }
+#pragma unroll 1
+            for (int t = 0; t < TT; t += 4) {
+                float y[4][4];
+                const int r0 = t + t / VE, r4 = t + 4 + (t + 4) / VE;  // rows of t and t + 4
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        f32x2 o = 0;
+                        const f32x2 dt = pack2(x[q].x, x[q].x), du = pack2(x[q].y, x[q].y);
+#pragma unroll
+                        for (int e = 0; e < NP; ++e) {
+                            const f32x2 a = G::kForm ? a1[q][G::kForm ? e : 0] : ex2_2(mul2(dt, A[q].v[e]));
+                            const f32x2 in = G::kForm ? b1[q][G::kForm ? e : 0] : mul2(du, bn.v[e]);
+                            const f32x2 c = G::kForm ? c1.v[e] : cn.v[e];
+                            h[q].v[e] = fma2(a, h[q].v[e], in);
+                            if (!ENDS) o = e ? fma2(h[q].v[e], c, o) : mul2(h[q].v[e], c);
+                        }
+                        const float2 f = unpack2(o);
+                        y[k][q] = f.x + f.y;
+                    }
+                    form();
+                    if (G::kForm)
+                        read(k < 2 ? r0 + k + 2 : r4 + k - 2);
+                    else
+                        read(k < 3 ? r0 + k + 1 : r4);
+                }
+                if (!ENDS) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        y[k][0] += __shfl_xor_sync(~0u, y[k][1], 1);
+                        y[k][2] += __shfl_xor_sync(~0u, y[k][3], 1);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[k][0] += __shfl_xor_sync(~0u, y[k][2], 2);
+                    *reinterpret_cast<float4 *>(out + t) =
+                        make_float4(y[0][0], y[1][0], y[2][0], y[3][0]);
+                }
+            }
+            if (i & 1)
+                barrier_arrive<kEmpty + 1>();
+            else
+                barrier_arrive<kEmpty>();
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (mine[q] >= c_count) continue;
+            if (ENDS)
+                h[q].store(p.h_chunk + (chunk_rows + mine[q]) * p.S, s0, p.S);
+            else if (p.final_state && chunk == p.chunks - 1)
+                h[q].store(p.final_state + (rows + mine[q]) * p.S, s0, p.S);
+        }
+        return;
+    }
+
+    // the rows: a lane has the positions t_mine .. of its warp's channels row, row + 8
+    const int quarter = lane & 3, t_mine = quarter * VE, half = warp - 1;
+    const int row = half * 16 + (lane >> 2);
+    const T *ub = static_cast<const T *>(p.u) + n * p.u_sn + (c_base + row) * p.u_sc;
+    const T *db = static_cast<const T *>(p.delta) + n * p.d_sn + (c_base + row) * p.d_sc;
+    const T *zb = !ENDS && p.z ? static_cast<const T *>(p.z) + n * p.z_sn + (c_base + row) * p.z_sc
                                : nullptr;
     const T *Bb = static_cast<const T *>(p.B) + n * p.b_sn + g * p.b_sg;
     const T *Cb = static_cast<const T *>(p.C) + n * p.c_sn + g * p.c_sg;
-
-    Pairs<SPT> A[2], h[2];
-    int mine[2];  // the pair's channels in the block
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        mine[k] = pair + k * G::PAIRS;
-        const int S = mine[k] < c_count ? p.S : 0;
-        A[k].load(p.A + (c_base + mine[k]) * p.S, s0, S);
-        A[k].scale(kLog2e);
-        if (ENDS)
-            h[k].fill(0.f);
-        else if (p.chunks > 1)
-            h[k].load(p.h_chunk + (chunk_rows + mine[k]) * p.S, s0, S);
-        else if (p.state)
-            h[k].load(p.state + (rows + mine[k]) * p.S, s0, S);
-        else
-            h[k].fill(0.f);
-    }
+    T *yb = static_cast<T *>(p.y) + (rows + row) * p.L;
     float bias[NI], D[NI], total[NI];
     int row_end[NI];
 #pragma unroll
     for (int k = 0; k < NI; ++k) {
-        const int c = lane / 4 + 8 * k;
+        const int c = row + 8 * k;
         row_end[k] = c < c_count ? end : 0;
         bias[k] = p.delta_bias && c < c_count ? p.delta_bias[c_base + c] : 0.f;
         D[k] = p.D && c < c_count ? p.D[c_base + c] : 0.f;
         total[k] = 0.f;
     }
-
-    Run<T, VE> u[NI], un[NI], dn[NI], z[NI], bcn[NB];
-    auto fetch_bc = [&](int t0) {
+    struct Next {
+        Run<T, VE> u[NI], d[NI], bc[NB];
+    } next[2];  // on their way: the tiles that the buffers will hold
+    struct Kept {
+        Run<T, VE> u[NI], z[NI];
+    } kept[2];  // of the tiles in the buffers
+    auto fetch_bc = [&](int t0, Run<T, VE> (&bc)[NB]) {
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int i = lane + 32 * k, s = i % SP, q = (i / SP) % 4, which = i / (SP * 4);
+            const int i = lane + 32 * half + 64 * k, s = i % SP, q = (i / SP) % 4, which = i / (SP * 4);
             if (ENDS && which) continue;
-            const T *row = which ? Cb + s * p.c_ss : Bb + s * p.b_ss;
-            load_run(bcn[k], row, t0 + q * VE, s < p.S ? end : 0, p.vec);
+            const T *from = which ? Cb + s * p.c_ss : Bb + s * p.b_ss;
+            load_run(bc[k], from, t0 + q * VE, s < p.S && which < 2 ? end : 0, p.vec);
         }
     };
-    auto fetch = [&](int t0) {
+    auto fetch = [&](int t0, Next &to) {
 #pragma unroll
         for (int k = 0; k < NI; ++k) {
-            const int c = lane / 4 + 8 * k;
-            load_run(dn[k], db + c * p.d_sc, t0 + t_mine, row_end[k], p.vec);
-            load_run(un[k], ub + c * p.u_sc, t0 + t_mine, row_end[k], p.vec);
+            load_run(to.d[k], db + 8 * k * p.d_sc, t0 + t_mine, row_end[k], p.vec);
+            load_run(to.u[k], ub + 8 * k * p.u_sc, t0 + t_mine, row_end[k], p.vec);
         }
-        if (G::kAhead) fetch_bc(t0);
+        if (G::kAhead) fetch_bc(t0, to.bc);
     };
-    if (first < end) fetch(first);
-    for (int t0 = first; t0 < end; t0 += TT) {
-        if (!G::kAhead) fetch_bc(t0);
+    auto stage = [&](int t0, float *buffer, Next &from, Kept &keep) {
+        if (!G::kAhead) fetch_bc(t0, from.bc);
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-            const int i = lane + 32 * k, s = i % SP, q = (i / SP) % 4, which = i / (SP * 4);
-            if (ENDS && which) continue;
-            float *to = bc + which * G::kMatrix + q * (VE + 1) * SP + s;
+            const int i = lane + 32 * half + 64 * k, s = i % SP, q = (i / SP) % 4, which = i / (SP * 4);
+            if (which >= (ENDS ? 1 : 2)) continue;
+            float *to = buffer + which * G::kMatrix + q * (VE + 1) * SP + s;
 #pragma unroll
-            for (int e = 0; e < VE; ++e) to[e * SP] = bcn[k][e];
+            for (int e = 0; e < VE; ++e) to[e * SP] = from.bc[k][e];
+        }
+        float dt[NI][VE];
+#pragma unroll
+        for (int k = 0; k < NI; ++k)
+#pragma unroll
+            for (int e = 0; e < VE; ++e) dt[k][e] = from.d[k][e] + bias[k];
+        if (p.softplus) {
+#pragma unroll
+            for (int k = 0; k < NI; ++k)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) dt[k][e] = softplus(dt[k][e]);
         }
 #pragma unroll
         for (int k = 0; k < NI; ++k) {
-            const int c = lane / 4 + 8 * k;
-            float2 *to = reinterpret_cast<float2 *>(steps) +
-                         ((c % G::PAIRS) * G::kStepPitch + quarter * (VE + 1)) * 2 + c / G::PAIRS;
-            u[k] = un[k];
-            float dt[VE];
+            float2 *to = reinterpret_cast<float2 *>(buffer + 2 * G::kMatrix) +
+                         (lane >> 2) * G::kStepPitch + quarter * (VE + 1) * 5 + 2 * half + k;
+            keep.u[k] = from.u[k];
+            if (t0 + TT > row_end[k]) {
+                // behind the end a step of size zero leaves the states as they are
 #pragma unroll
-            for (int e = 0; e < VE; ++e) dt[e] = dn[k][e] + bias[k];
-            if (p.softplus) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) dt[e] = softplus(dt[e]);
+                for (int e = 0; e < VE; ++e) dt[k][e] = t0 + t_mine + e < row_end[k] ? dt[k][e] : 0.f;
             }
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                to[2 * e] = make_float2(dt[e], dt[e] * u[k][e]);
-                if (ENDS) total[k] += t0 + t_mine + e < row_end[k] ? dt[e] : 0.f;
+                to[5 * e] = make_float2(dt[k][e], dt[k][e] * keep.u[k][e]);
+                if (ENDS) total[k] += dt[k][e];
             }
         }
-        if (t0 + TT > end || c_count < G::CW) {
-            // behind the end a step of size zero leaves the states as they are
-            __syncwarp();
-            for (int i = lane; i < G::CW * TT; i += 32) {
-                const int c = i / TT, t = i % TT;
-                if (t0 + t >= end || c >= c_count)
-                    reinterpret_cast<float2 *>(steps)[((c % G::PAIRS) * G::kStepPitch + t + t / VE) * 2 +
-                                                      c / G::PAIRS] = make_float2(0.f, 0.f);
+    };
+    auto finish = [&](int t0, const float *buffer, const Kept &keep) {
+        float o[NI][VE];
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+            const float4 *q = reinterpret_cast<const float4 *>(
+                buffer + 2 * G::kMatrix + G::kSteps + (2 * half + k) * G::kOutPart +
+                (lane >> 2) * G::kOutPitch + t_mine);
+#pragma unroll
+            for (int e = 0; e < VE; e += 4) {
+                const float4 f = q[e / 4];
+                const float y[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[k][e + i] = fmaf(D[k], keep.u[k][e + i], y[i]);
             }
         }
-        __syncwarp();
-        if (t0 + TT < end) fetch(t0 + TT);
-        if (!ENDS && zb) {
+        if (zb) {
 #pragma unroll
             for (int k = 0; k < NI; ++k)
-                load_run(z[k], zb + (lane / 4 + 8 * k) * p.z_sc, t0 + t_mine, row_end[k], p.vec);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) o[k][e] *= silu(keep.z[k][e]);
         }
-        const float4 *step = reinterpret_cast<const float4 *>(steps) + pair * G::kStepPitch;
-        // Two positions ahead of the states, what a position needs is read; one
-        // ahead, its decays and inputs are formed: a warp has few neighbours to
-        // hide a latency behind.  (Behind the tile's last position lie rows that
-        // are read and not used.)
-        float4 xn = step[0];
-        Pairs<SPT> bn, cn, c1;
-        bn.read(bc + s0);
-        if (!ENDS) cn.read(bc + G::kMatrix + s0);
-        f32x2 a1[2][NP], b1[2][NP];
-        auto advance = [&](int r) {  // forms the position that was read, reads row r
-            const f32x2 dt[2] = {pack2(xn.x, xn.x), pack2(xn.z, xn.z)};
-            const f32x2 du[2] = {pack2(xn.y, xn.y), pack2(xn.w, xn.w)};
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
+        for (int k = 0; k < NI; ++k) {
+            if (t0 + TT > end) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    a1[q][i] = ex2_2(mul2(dt[q], A[q].v[i]));
-                    b1[q][i] = mul2(du[q], bn.v[i]);
-                }
+                for (int e = 0; e < VE; ++e) o[k][e] = t0 + t_mine + e < end ? o[k][e] : 0.f;
             }
-            c1 = cn;
-            xn = step[r];
-            bn.read(bc + r * SP + s0);
-            if (!ENDS) cn.read(bc + G::kMatrix + r * SP + s0);
-        };
-        advance(1);
-#pragma unroll 1
-        for (int t = 0; t < TT; t += 4) {
-            float out[4][2];
-            const int r0 = t + t / VE, r4 = t + 4 + (t + 4) / VE;  // rows of t and t + 4
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                f32x2 y[2];
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        h[q].v[i] = fma2(a1[q][i], h[q].v[i], b1[q][i]);
-                        if (!ENDS) y[q] = i ? fma2(h[q].v[i], c1.v[i], y[q]) : mul2(h[q].v[i], c1.v[i]);
-                    }
-                }
-                advance(k < 2 ? r0 + k + 2 : r4 + k - 2);
-                if (!ENDS) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float2 f = unpack2(y[q]);
-                        out[k][q] = f.x + f.y;
-                    }
-                }
-            }
-            if (!ENDS) {
-                // even lanes keep the pair's first channel, odd lanes the second
-                float w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[k] = (j & 1 ? out[k][1] : out[k][0]) +
-                           __shfl_xor_sync(~0u, j & 1 ? out[k][0] : out[k][1], 1);
-                if (LPC == 4) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) w[k] += __shfl_xor_sync(~0u, w[k], 2);
-                }
-                if (j < 2)
-                    *reinterpret_cast<float4 *>(outs + j * G::kOutHalf + pair * G::kOutPitch + t) =
-                        make_float4(w[0], w[1], w[2], w[3]);
-            }
+            Run<T, VE> out;
+            out.put(o[k]);
+            if (row + 8 * k < c_count)
+                store_run(out, yb + 8 * k * (int64_t)p.L, t0 + t_mine, stop, p.vec_y);
         }
-        __syncwarp();
-        if constexpr (!ENDS) {
+    };
+    if (tiles > 0) fetch(first, next[0]);
+    if (tiles > 1) fetch(first + TT, next[1]);
+    for (int i0 = 0; i0 < tiles + 2; i0 += 2) {
 #pragma unroll
-            for (int k = 0; k < NI; ++k) {
-                const int c = lane / 4 + 8 * k;
-                const float4 *q = reinterpret_cast<const float4 *>(
-                    outs + c / G::PAIRS * G::kOutHalf + c % G::PAIRS * G::kOutPitch + t_mine);
-                float o[VE];
-#pragma unroll
-                for (int e = 0; e < VE; e += 4) {
-                    const float4 f = q[e / 4];
-                    const float y[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[e + i] = fmaf(D[k], u[k][e + i], y[i]);
-                }
-                if (zb) {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) o[e] *= silu(z[k][e]);
-                }
-                if (t0 + TT > end)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) o[e] = t0 + t_mine + e < end ? o[e] : 0.f;
-                Run<T, VE> out;
-                out.put(o);
-                if (c < c_count)
-                    store_run(out, static_cast<T *>(p.y) + (rows + c) * p.L, t0 + t_mine, stop, p.vec_y);
+        for (int b = 0; b < 2; ++b) {  // (by pairs, so that what is kept stays in registers)
+            const int i = i0 + b, t0 = first + i * TT;
+            float *buffer = sm + b * G::kBuffer;
+            if (i >= 2 && i - 2 < tiles) {
+                if (b)
+                    barrier_sync<kEmpty + 1>();
+                else
+                    barrier_sync<kEmpty>();
+                if (!ENDS) finish(t0 - 2 * TT, buffer, kept[b]);
             }
+            if (i >= tiles) continue;
+            __syncwarp();
+            stage(t0, buffer, next[b], kept[b]);
+            if (b)
+                barrier_arrive<kFull + 1>();
+            else
+                barrier_arrive<kFull>();
+            if (!ENDS && zb) {
+#pragma unroll
+                for (int k = 0; k < NI; ++k)
+                    load_run(kept[b].z[k], zb + 8 * k * p.z_sc, t0 + t_mine, row_end[k], p.vec);
+            }
+            if (i + 2 < tiles) fetch(t0 + 2 * TT, next[b]);
         }
     }
     if (ENDS) {
@@ -275,27 +353,18 @@ __global__ void __launch_bounds__(32) scan_kernel(const ScanParams p) {
         for (int k = 0; k < NI; ++k) {
             total[k] += __shfl_xor_sync(~0u, total[k], 1);
             total[k] += __shfl_xor_sync(~0u, total[k], 2);
-            const int c = lane / 4 + 8 * k;
-            if (quarter == 0 && c < c_count) p.dt_chunk[chunk_rows + c] = total[k];
+            if (quarter == 0 && row + 8 * k < c_count) p.dt_chunk[chunk_rows + row + 8 * k] = total[k];
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (mine[k] < c_count) h[k].store(p.h_chunk + (chunk_rows + mine[k]) * p.S, s0, p.S);
         return;
     }
     // positions of the chunk behind the last tile
-    const int done = first + (end - first + TT - 1) / TT * TT;
+    const int done = first + tiles * TT;
     if (done < stop) {
         Run<T, VE> zero;
         zero.clear();
-        for (int c = lane / 4; c < c_count; c += 8)
-            for (int t = done + t_mine; t < stop; t += TT)
-                store_run(zero, static_cast<T *>(p.y) + (rows + c) * p.L, t, stop, p.vec_y);
-    }
-    if (p.final_state && chunk == p.chunks - 1) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (mine[k] < c_count) h[k].store(p.final_state + (rows + mine[k]) * p.S, s0, p.S);
+        for (int k = 0; k < NI; ++k)
+            for (int t = done + t_mine; t < stop && row + 8 * k < c_count; t += TT)
+                store_run(zero, yb + 8 * k * (int64_t)p.L, t, stop, p.vec_y);
     }
 }
 
@@ -514,30 +583,25 @@ bool elements(size_t e, std::initializer_list<const void *> ps) {
 
 namespace {
 
-constexpr int64_t kSplitBelow = 304, kSplitTo = 1216;  // warps
+constexpr int64_t kSplitBelow = kSMs, kSplitTo = 4 * kSMs;  // blocks
 
-// f(SPT, LPC) for the smallest tile that holds S states.
+// f(SPT, LPC) for the smallest tile of a step that holds S states.
 template <typename F>
-int by_tile(int S, bool wide, F f) {
+int by_lanes(int S, F f) {
     using std::integral_constant;
     if (S <= 4) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
     if (S <= 8) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-    if (S <= 16)
-        return wide ? f(integral_constant<int, 8>{}, integral_constant<int, 2>{})
-                    : f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    if (S <= 16) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
     if (S <= 32) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
     return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
 }
 
-// Blocks and chunks of the forward scan.  One pass over a sequence needs a warp
-// per 32 channels of each sequence; where that leaves schedulers idle the
-// sequence is cut, into chunks of 128 positions at least.  Two more
-// passes over the states are the price: what every chunk leaves from zero (no
-// outputs), and the join.
+// Blocks and chunks of the forward scan.  One pass over a sequence needs a block
+// per 32 channels of each sequence; where that leaves SMs idle the sequence is
+// cut, into chunks of 128 positions at least.  Two more passes over the states
+// are the price: what every chunk leaves from zero (no outputs), and the join.
 void plan_chunks(ScanParams &p) {
-    p.wide = (int64_t)p.N * p.channels >= 16 * 4096;
-    const int cw = p.S <= 8 || p.S > 16 && p.S <= 32 || p.S <= 16 && p.wide ? 32 : 16;
-    p.blocks_per_group = (p.per_group + cw - 1) / cw;
+    p.blocks_per_group = (p.per_group + 31) / 32;
     const int64_t blocks = (int64_t)p.groups * p.blocks_per_group * p.N;
     const int64_t most = p.L / 128;
     p.chunks = 1;
@@ -600,16 +664,21 @@ SPCONV_API int spconv_scan(const spconv_scan_args *a, void *stream) {
     p.vec_y = rows_aligned(a->y, 0, L, e);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return by_dtype(a->dtype, [&](auto t) {
-        return by_tile(a->S, p.wide, [&](auto spt, auto lpc) {
+        return by_states(a->S, [&](auto spt) {
             using T = decltype(t);
-            constexpr int SPT = decltype(spt)::value, LPC = decltype(lpc)::value;
+            constexpr int SPT = decltype(spt)::value, smem = 2 * ScanTile<T, SPT>::kBuffer * 4;
+            static_assert(smem <= 227 * 1024, "two tiles fit shared memory");
             const dim3 grid(p.groups * p.blocks_per_group, p.N, p.chunks);
+            auto *ends = scan_kernel<T, SPT, true>;
+            auto *full = scan_kernel<T, SPT, false>;
+            if (int rc = raise_smem(reinterpret_cast<const void *>(full), smem)) return rc;
             if (p.chunks > 1) {
-                scan_kernel<T, SPT, LPC, true><<<grid, 32, 0, s>>>(p);
+                if (int rc = raise_smem(reinterpret_cast<const void *>(ends), smem)) return rc;
+                ends<<<grid, kScanThreads, smem, s>>>(p);
                 if (int rc = launch_status()) return rc;
                 if (int rc = scan_join_chunks(p, false, s)) return rc;
             }
-            scan_kernel<T, SPT, LPC, false><<<grid, 32, 0, s>>>(p);
+            full<<<grid, kScanThreads, smem, s>>>(p);
             return launch_status();
         });
     });
@@ -645,7 +714,7 @@ SPCONV_API int spconv_scan_step(const spconv_scan_args *a, void *stream) {
             rows_aligned(a->B, a->b_stride_n, a->b_stride_g, e) &&
             rows_aligned(a->C, a->c_stride_n, a->c_stride_g, e);
     return by_dtype(a->dtype, [&](auto t) {
-        return by_tile(a->S, true, [&](auto spt, auto lpc) {
+        return by_lanes(a->S, [&](auto spt, auto lpc) {
             constexpr int SPT = decltype(spt)::value, LPC = decltype(lpc)::value, CB = 256 / LPC;
             const int64_t blocks = ((int64_t)a->channels + CB - 1) / CB;
             int64_t side = (4 * kSMs + blocks - 1) / blocks;  // requests side by side: 4 blocks per SM

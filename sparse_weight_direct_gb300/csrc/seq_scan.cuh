@@ -26,7 +26,6 @@ struct ScanParams {
     int softplus, num_slots;
     int chunks, chunk_len;         // chunk_len: a multiple of the tile
     int tiles, segments, tiles_per_segment;  // backward
-    int wide;                      // forward: the tile with fewer lanes per channel
     int vec;                       // input rows can be read as vectors
     int vec_y;                     // output rows (N x channels x L) likewise
 };
