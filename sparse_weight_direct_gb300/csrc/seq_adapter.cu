@@ -37,6 +37,9 @@ struct AdapterParams {
     int vec_x, vec_a, vec_b, vec_y;  // rows can be read 16 (b of prompts: 4) bytes at a time
 };
 
+constexpr int kMaxRanks = 8;  // blocks of a cluster
+constexpr int kMaxR = 64;
+
 static __device__ __forceinline__ int adapter_of(const AdapterParams &p, int64_t n) {
     const int i = p.index[n];
     return i >= 0 && i < p.adapters ? i : -1;
@@ -405,13 +408,18 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         // each block adds a share of v over the ranks and hands it to all
         for (int i = rank * kThreads + threadIdx.x; i < G::RP * kPos / 4; i += ranks * kThreads) {
             const int o = i / (kPos / 4) * G::kVPitch + i % (kPos / 4) * 4;
-            float4 t = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(part, 0) + o);
-            for (int k = 1; k < ranks; ++k) {
-                const float4 f = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(part, k) + o);
-                t.x += f.x; t.y += f.y; t.z += f.z; t.w += f.w;
+            float4 f[kMaxRanks], t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMaxRanks; ++k)  // read together, added in their order
+                f[k] = k < ranks ? *reinterpret_cast<const float4 *>(cluster.map_shared_rank(part, k) + o)
+                                 : t;
+#pragma unroll
+            for (int k = 0; k < kMaxRanks; ++k) {
+                t.x += f[k].x; t.y += f[k].y; t.z += f[k].z; t.w += f[k].w;
             }
-            for (int k = 0; k < ranks; ++k)
-                *reinterpret_cast<float4 *>(cluster.map_shared_rank(v, k) + o) = t;
+#pragma unroll
+            for (int k = 0; k < kMaxRanks; ++k)
+                if (k < ranks) *reinterpret_cast<float4 *>(cluster.map_shared_rank(v, k) + o) = t;
         }
         cluster.sync();
     } else {
@@ -530,8 +538,6 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
 // ---------------------------------------------------------------- single tokens
 
 constexpr int kTokenThreads = 256, kTokenWarps = kTokenThreads / 32;
-constexpr int kMaxRanks = 8;
-constexpr int kMaxR = 64;
 
 // A cluster per token.  A warp sums two rows of a at a time over the block's
 // channels, every block adds the ranks' parts of v, a thread sums rows of b.
@@ -605,8 +611,14 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const AdapterParam
     cluster.sync();
     if (threadIdx.x < kMaxR) {
         float t = 0.f;
-        if (threadIdx.x < p.R)
-            for (int k = 0; k < ranks; ++k) t += cluster.map_shared_rank(part, k)[threadIdx.x];
+        if (threadIdx.x < p.R) {
+            float f[kMaxRanks];  // read together, added in their order
+#pragma unroll
+            for (int k = 0; k < kMaxRanks; ++k)
+                f[k] = k < ranks ? cluster.map_shared_rank(part, k)[threadIdx.x] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxRanks; ++k) t += f[k];
+        }
         v[threadIdx.x] = t;
     }
     __syncthreads();
