@@ -234,34 +234,41 @@ static __device__ __forceinline__ float sum4(float v) {
     return v + __shfl_xor_sync(~0u, v, 2);
 }
 
-// Sums v[matrix][state] over the eight pairs of a warp (lane bits 4, 3, 2): at
+// Sums v[position][matrix][state] over the eight pairs of a warp (lane bits 4, 3, 2): at
 // each bit the lanes give half of what they hold to each other, states first,
 // then the matrices, so that every lane ends with its own share of the sums
-// (v[0 .. MATS)[0 .. N)), the first state of which is `state`, of matrix `mat`.
-template <int SPT, int MATS, int N, int BIT>
+// (v[k][0 .. MATS)[0 .. N)), the first state of which is `state`, of matrix `mat`.
+template <int SPT, int MATS, int N, int BIT, int Q>
 struct PairSum {
-    static __device__ __forceinline__ void run(float (&v)[2][SPT], int lane, int &state, int &mat) {
+    static __device__ __forceinline__ void run(float (&v)[Q][2][SPT], int lane, int &state, int &mat) {
         if constexpr (BIT >= 4) {
             const bool up = lane & BIT;
             if constexpr (N > 1) {
 #pragma unroll
-                for (int w = 0; w < MATS; ++w)
+                for (int k = 0; k < Q; ++k)
 #pragma unroll
-                    for (int i = 0; i < N / 2; ++i) {
-                        const float keep = up ? v[w][i + N / 2] : v[w][i];
-                        const float give = up ? v[w][i] : v[w][i + N / 2];
-                        v[w][i] = keep + __shfl_xor_sync(~0u, give, BIT);
-                    }
+                    for (int w = 0; w < MATS; ++w)
+#pragma unroll
+                        for (int i = 0; i < N / 2; ++i) {
+                            const float keep = up ? v[k][w][i + N / 2] : v[k][w][i];
+                            const float give = up ? v[k][w][i] : v[k][w][i + N / 2];
+                            v[k][w][i] = keep + __shfl_xor_sync(~0u, give, BIT);
+                        }
                 state += up ? N / 2 : 0;
-                PairSum<SPT, MATS, N / 2, BIT / 2>::run(v, lane, state, mat);
+                PairSum<SPT, MATS, N / 2, BIT / 2, Q>::run(v, lane, state, mat);
             } else if constexpr (MATS > 1) {
-                const float keep = up ? v[1][0] : v[0][0], give = up ? v[0][0] : v[1][0];
-                v[0][0] = keep + __shfl_xor_sync(~0u, give, BIT);
+#pragma unroll
+                for (int k = 0; k < Q; ++k) {
+                    const float keep = up ? v[k][1][0] : v[k][0][0];
+                    const float give = up ? v[k][0][0] : v[k][1][0];
+                    v[k][0][0] = keep + __shfl_xor_sync(~0u, give, BIT);
+                }
                 mat = up;
-                PairSum<SPT, 1, 1, BIT / 2>::run(v, lane, state, mat);
+                PairSum<SPT, 1, 1, BIT / 2, Q>::run(v, lane, state, mat);
             } else {
-                v[0][0] += __shfl_xor_sync(~0u, v[0][0], BIT);
-                PairSum<SPT, 1, 1, BIT / 2>::run(v, lane, state, mat);
+#pragma unroll
+                for (int k = 0; k < Q; ++k) v[k][0][0] += __shfl_xor_sync(~0u, v[k][0][0], BIT);
+                PairSum<SPT, 1, 1, BIT / 2, Q>::run(v, lane, state, mat);
             }
         }
     }
@@ -321,24 +328,30 @@ __global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams
         // forwards: the states before every Q positions
 #pragma unroll 1
         for (int m = 0; m < TT / Q; ++m) {
+            // (what the positions need is read before the states are stored: a store
+            // holds later reads back)
+            const int r0 = G::row(m * Q);  // (Q divides VE)
+            Pairs<SPT> b[Q];
+            float2 x[Q][2];
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                b[k].read(at.bc + (r0 + k) * SP + s0);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) x[k][q] = step[q][(r0 + k) * 2];
+            }
             f32x2 *to = reinterpret_cast<f32x2 *>(kept + m * G::kKept) + lane;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int i = 0; i < NP; ++i) to[(q * NP + i) * 32] = h[q].v[i];
-            if (m == TT / Q - 1) break;
 #pragma unroll
             for (int k = 0; k < Q; ++k) {
-                const int r = G::row(m * Q) + k;  // (Q divides VE)
-                Pairs<SPT> b;
-                b.read(at.bc + r * SP + s0);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float2 x = step[q][r * 2];
-                    const f32x2 dt = pack2(x.x, x.x), du = pack2(x.y, x.y);
+                    const f32x2 dt = pack2(x[k][q].x, x[k][q].x), du = pack2(x[k][q].y, x[k][q].y);
 #pragma unroll
                     for (int i = 0; i < NP; ++i)
-                        h[q].v[i] = fma2(ex2_2(mul2(dt, A[q].v[i])), h[q].v[i], mul2(du, b.v[i]));
+                        h[q].v[i] = fma2(ex2_2(mul2(dt, A[q].v[i])), h[q].v[i], mul2(du, b[k].v[i]));
                 }
             }
         }
@@ -349,7 +362,7 @@ __global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams
             f32x2 hs[Q + 1][2][NP], a[Q][2][NP];
             Pairs<SPT> b[Q], c[Q];
             float2 x[Q][2];
-            float y[Q][2];
+            float y[Q][2], of[Q][2];
             const f32x2 *from = reinterpret_cast<const f32x2 *>(kept + m * G::kKept) + lane;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -362,6 +375,7 @@ __global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     x[k][q] = step[q][(r0 + k) * 2];
+                    of[k][q] = dos[q][(r0 + k) * 2];
                     const f32x2 dt = pack2(x[k][q].x, x[k][q].x), du = pack2(x[k][q].y, x[k][q].y);
                     f32x2 o = 0;
 #pragma unroll
@@ -374,26 +388,15 @@ __global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams
                     y[k][q] = f.x + f.y;
                 }
             }
-            __syncwarp();  // the kept states of all lanes have been read: their place is used again
-#pragma unroll
-            for (int k = 0; k < Q; ++k) {
-                y[k][0] += __shfl_xor_sync(~0u, y[k][1], 1);
-                y[k][0] += __shfl_xor_sync(~0u, y[k][0], 2);
-            }
-            float *out = outs + odd * G::kOutHalf + pair * G::kOutPitch + m * Q;
-            if (j < 2) {
-#pragma unroll
-                for (int k = 0; k < Q; ++k) out[k] = y[k][0];
-            }
-            float share[Q];
+            // The sums over lanes wait for each other and the stores for them, so they
+            // come behind the Q positions, those of all positions side by side.
+            float s1[Q][2], s2[Q][2], v[Q][2][SPT];
 #pragma unroll
             for (int k = Q - 1; k >= 0; --k) {
                 f32x2 vB[NP], vC[NP];
-                float s1[2], s2[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float of = dos[q][(r0 + k) * 2];
-                    const f32x2 o = pack2(of, of), du = pack2(x[k][q].y, x[k][q].y);
+                    const f32x2 o = pack2(of[k][q], of[k][q]), du = pack2(x[k][q].y, x[k][q].y);
                     const f32x2 dt = pack2(x[k][q].x, x[k][q].x);
                     f32x2 gB = 0, qA = 0;
 #pragma unroll
@@ -408,31 +411,48 @@ __global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams
                         dA[q].v[i] = fma2(w, dt, dA[q].v[i]);
                     }
                     const float2 f1 = unpack2(gB), f2 = unpack2(qA);
-                    s1[q] = f1.x + f1.y;
-                    s2[q] = f2.x + f2.y;
+                    s1[k][q] = f1.x + f1.y;
+                    s2[k][q] = f2.x + f2.y;
                 }
-                // lanes 0, 1 of the pair end with g . B, lanes 2, 3 with q . A
-                s1[0] += __shfl_xor_sync(~0u, s1[1], 1);
-                s2[0] += __shfl_xor_sync(~0u, s2[1], 1);
-                share[k] = (j & 2 ? s2[0] : s1[0]) + __shfl_xor_sync(~0u, j & 2 ? s1[0] : s2[0], 2);
-                float v[2][SPT];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const float2 fB = unpack2(vB[i]), fC = unpack2(vC[i]);
-                    v[0][2 * i < SPT ? 2 * i : 0] = fB.x;
-                    v[1][2 * i < SPT ? 2 * i : 0] = fC.x;
+                    v[k][0][2 * i < SPT ? 2 * i : 0] = fB.x;
+                    v[k][1][2 * i < SPT ? 2 * i : 0] = fC.x;
                     if constexpr (SPT > 1) {
-                        v[0][2 * i + 1] = fB.y;
-                        v[1][2 * i + 1] = fC.y;
+                        v[k][0][2 * i + 1] = fB.y;
+                        v[k][1][2 * i + 1] = fC.y;
                     }
                 }
-                int state = s0, mat = 0;
-                PairSum<SPT, 2, SPT, 16>::run(v, lane, state, mat);
+            }
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                y[k][0] += __shfl_xor_sync(~0u, y[k][1], 1);
+                s1[k][0] += __shfl_xor_sync(~0u, s1[k][1], 1);
+                s2[k][0] += __shfl_xor_sync(~0u, s2[k][1], 1);
+            }
+            float share[Q];  // lanes 0, 1 of the pair end with g . B, lanes 2, 3 with q . A
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                y[k][0] += __shfl_xor_sync(~0u, y[k][0], 2);
+                share[k] = (j & 2 ? s2[k][0] : s1[k][0]) +
+                           __shfl_xor_sync(~0u, j & 2 ? s1[k][0] : s2[k][0], 2);
+            }
+            int state = s0, mat = 0;
+            PairSum<SPT, 2, SPT, 16, Q>::run(v, lane, state, mat);
+            __syncwarp();  // the kept states of all lanes have been read: their place is used again
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
                 float *to = kept + m * G::kKept + k * 2 * SP + mat * SP + state;
 #pragma unroll
                 for (int w = 0; w < PairShare<SPT>::MATS; ++w)
 #pragma unroll
-                    for (int i = 0; i < PairShare<SPT>::N; ++i) to[w * SP + i] = v[w][i];
+                    for (int i = 0; i < PairShare<SPT>::N; ++i) to[w * SP + i] = v[k][w][i];
+            }
+            float *out = outs + odd * G::kOutHalf + pair * G::kOutPitch + m * Q;
+            if (j < 2) {
+#pragma unroll
+                for (int k = 0; k < Q; ++k) out[k] = y[k][0];
             }
             float *sums = outs + (1 + (j >> 1)) * G::kOut + odd * G::kOutHalf + pair * G::kOutPitch + m * Q;
 #pragma unroll
