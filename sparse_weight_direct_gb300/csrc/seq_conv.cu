@@ -183,12 +183,13 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParam
         n = first / p.runs;
         run = first - (int)n * p.runs;
     }
-    for (; n < p.N && p.runs > 0; ) {
+    int64_t rowi = n * p.C + c;
+    const T *row = static_cast<const T *>(p.x) + n * p.x_sn + c * p.x_sc;
+    const T *drow = static_cast<const T *>(p.dy) + n * p.dy_sn + c * p.dy_sc;
+    const int64_t x_step = dn * p.x_sn, dy_step = dn * p.dy_sn, row_step = (int64_t)dn * p.C;
+    while (n < p.N && p.runs > 0) {
         const int t0 = run * kVec;
         const int len = length_of(p.lengths, (int)n, p.L);
-        const int64_t rowi = n * p.C + c;
-        const T *row = static_cast<const T *>(p.x) + n * p.x_sn + c * p.x_sc;
-        const T *drow = static_cast<const T *>(p.dy) + n * p.dy_sn + c * p.dy_sc;
         const T *st = p.state ? static_cast<const T *>(p.state) + rowi * (K - 1) : nullptr;
         const T *df = p.dfinal ? static_cast<const T *>(p.dfinal) + rowi * (K - 1) : nullptr;
         constexpr int kG = kVec + K - 1;
@@ -259,10 +260,16 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParam
             }
         }
         n += dn;
+        row += x_step;
+        drow += dy_step;
+        rowi += row_step;
         run += dr;
         if (run >= p.runs) {
             run -= p.runs;
             ++n;
+            row += p.x_sn;
+            drow += p.dy_sn;
+            rowi += p.C;
         }
     }
     __shared__ float part[kThreads / 32][K + 1];
