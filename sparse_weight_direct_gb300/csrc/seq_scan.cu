@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kScanThreads, SPT <= 4 ? 4 : 2) scan_kernel(co
                         const f32x2 dt = pack2(x[q].x, x[q].x), du = pack2(x[q].y, x[q].y);
 #pragma unroll
                         for (int k = 0; k < NP; ++k) {
-                            a1[q][k] = ex2_2(mul2(dt, A[q].v[k]));
+                            a1[q][k] = decay2(dt, A[q].v[k]);
                             b1[q][k] = mul2(du, bn.v[k]);
                         }
                     }
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kScanThreads, SPT <= 4 ? 4 : 2) scan_kernel(co
                         const f32x2 dt = pack2(x[q].x, x[q].x), du = pack2(x[q].y, x[q].y);
 #pragma unroll
                         for (int e = 0; e < NP; ++e) {
-                            const f32x2 a = G::kForm ? a1[q][G::kForm ? e : 0] : ex2_2(mul2(dt, A[q].v[e]));
+                            const f32x2 a = G::kForm ? a1[q][G::kForm ? e : 0] : decay2(dt, A[q].v[e]);
                             const f32x2 in = G::kForm ? b1[q][G::kForm ? e : 0] : mul2(du, bn.v[e]);
                             const f32x2 c = G::kForm ? c1.v[e] : cn.v[e];
                             h[q].v[e] = fma2(a, h[q].v[e], in);
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
             const float du = dt * now.u;
 #pragma unroll
             for (int k = 0; k < SPT; ++k) {
-                now.h[k] = fmaf(ex2(dt * A[k]), now.h[k], du * now.b[k]);
+                now.h[k] = fmaf(decay(dt, A[k]), now.h[k], du * now.b[k]);
                 o = fmaf(now.h[k], now.c[k], o);
             }
             if constexpr (SPT % 4 == 0) {

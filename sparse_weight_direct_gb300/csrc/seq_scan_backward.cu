@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kBackThreads) segment_ends_kernel(const ScanPa
             for (int i = 0; i < NP; ++i) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const f32x2 a = ex2_2(mul2(dt[q], A[q].v[i]));
+                    const f32x2 a = decay2(dt[q], A[q].v[i]);
                     h[q].v[i] = fma2(a, h[q].v[i], mul2(du[q], b.v[i]));
                     P[q].v[i] = mul2(P[q].v[i], a);
                     g[q].v[i] = fma2(mul2(P[q].v[i], c.v[i]), od[q], g[q].v[i]);
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams
                     const f32x2 dt = pack2(x[k][q].x, x[k][q].x), du = pack2(x[k][q].y, x[k][q].y);
 #pragma unroll
                     for (int i = 0; i < NP; ++i)
-                        h[q].v[i] = fma2(ex2_2(mul2(dt, A[q].v[i])), h[q].v[i], mul2(du, b[k].v[i]));
+                        h[q].v[i] = fma2(decay2(dt, A[q].v[i]), h[q].v[i], mul2(du, b[k].v[i]));
                 }
             }
         }
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams
                     f32x2 o = 0;
 #pragma unroll
                     for (int i = 0; i < NP; ++i) {
-                        a[k][q][i] = ex2_2(mul2(dt, A[q].v[i]));
+                        a[k][q][i] = decay2(dt, A[q].v[i]);
                         hs[k + 1][q][i] = fma2(a[k][q][i], hs[k][q][i], mul2(du, b[k].v[i]));
                         o = i ? fma2(hs[k + 1][q][i], c[k].v[i], o) : mul2(hs[k + 1][q][i], c[k].v[i]);
                     }

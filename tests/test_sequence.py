@@ -642,3 +642,25 @@ def test_refused_at_the_python_entry():
         with pytest.raises(swd.SpconvError):
             call()
             pytest.fail(f"call {i} was not refused")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("L", [40, 300, 1030])
+def test_positions_behind_the_end_leave_no_trace(dtype, L):
+    """A padded sequence gives the bits of the sequence alone, in outputs, states
+    and gradients, wherever its end lies in a tile or a chunk."""
+    s, dy, state, dfinal, _ = scan_inputs((1, 40, L, 16, 1), dtype, False, seed=20)
+    for k in (1, 7, 32, 33, L // 2 + 3, L - 1):
+        lens = torch.tensor([k], dtype=torch.int32, device="cuda")
+        cut = {n: v[..., :k].contiguous() if n in ("u", "delta", "B", "C", "z") else v for n, v in s.items()}
+        a, b = torch.empty_like(state), torch.empty_like(state)
+        y = swd.scan(**s, state=state, final_state=a, lengths=lens)
+        assert not y[..., k:].any()
+        # (cut into other chunks the states are joined at other places)
+        swd.scan(**cut, state=state, final_state=b)
+        tight = 2.0 ** -19 if L >= 256 else 0.0
+        assert float((a - b).abs().max()) <= tight * float(b.abs().max())
+        g = swd.scan_backward(dy, **s, state=state, dfinal_state=dfinal, lengths=lens)
+        for n in ("du", "ddelta", "dB", "dC", "dz"):
+            assert not g[n][..., k:].any(), n
