@@ -437,6 +437,8 @@ int spconv_packed_copy_array(const spconv_packed *p, int which, void *dst, int64
  *    bytes for the same arguments (pointers are not looked at); the workspace
  *    is 16-byte aligned device memory that the caller keeps until the stream
  *    has passed the call.
+ *  - Limits: K <= 4 taps, S <= 64 states, rank R <= 64, N <= 65535 for the scan
+ *    and the steps, C, M and P <= 2^26 for the adapters.
  *  - Errors: INVALID_ARG (a NULL or misaligned pointer, a negative size or
  *    stride, sizes that do not fit together, an output that overlaps an input,
  *    a workspace that is too small), UNSUPPORTED (a size beyond the kernels),
@@ -560,11 +562,8 @@ typedef struct spconv_adapter_args {
     const float *scale;            /* adapters, or NULL (all 1)                         */
     const void *y;                 /* N x M x P, contiguous                             */
     void *out;                     /* N x M x P; may be y itself                        */
-    void *workspace;
-    int64_t workspace_bytes;
 } spconv_adapter_args;
 
-int64_t spconv_adapter_workspace(const spconv_adapter_args *args);
 int spconv_adapter_add(const spconv_adapter_args *args, void *stream);
 
 #ifdef __cplusplus

@@ -35,7 +35,7 @@ EXPORTS = ("spconv_pack", "spconv_pack_ex", "spconv_forward", "spconv_forward_ex
            "spconv_short_conv_backward_workspace", "spconv_short_conv_step",
            "spconv_scan", "spconv_scan_workspace", "spconv_scan_backward",
            "spconv_scan_backward_workspace", "spconv_scan_step",
-           "spconv_adapter_add", "spconv_adapter_workspace")
+           "spconv_adapter_add")
 
 _lock = threading.Lock()
 _lib = None
@@ -105,8 +105,7 @@ class AdapterArgs(ctypes.Structure):
     _fields_ = _fields(
         (_i32, "N P C M R adapters dtype reserved"),
         (_i64, "x_stride_n x_stride_c"),
-        (_ptr, "x a b index scale y out workspace"),
-        (_i64, "workspace_bytes"))
+        (_ptr, "x a b index scale y out"))
 
 
 def lib() -> ctypes.CDLL:
@@ -158,7 +157,7 @@ def lib() -> ctypes.CDLL:
                   "scan_step", "adapter_add"):
             f = getattr(L, "spconv_" + n)
             f.argtypes, f.restype = [p, p], i
-        for n in ("short_conv_backward", "scan", "scan_backward", "adapter"):
+        for n in ("short_conv_backward", "scan", "scan_backward"):
             f = getattr(L, f"spconv_{n}_workspace")
             f.argtypes, f.restype = [p], ctypes.c_int64
         _lib = L

@@ -552,8 +552,10 @@ constexpr int kTokenThreads = 256, kTokenWarps = kTokenThreads / 32;
 // A cluster per token.  A warp sums two rows of a at a time over the block's
 // channels, every block adds the ranks' parts of v, a thread sums rows of b.
 // What does not depend on v -- the first rows of b, of y -- is read before it.
+// Three blocks fit an SM: 48 tokens' 384 run at once (7.1 us; two an SM 8.9, four with
+// fewer registers 9.5; 4096 x 4096, rank 16, bf16).
 template <typename T>
-__global__ void __launch_bounds__(kTokenThreads) token_kernel(const AdapterParams p) {
+__global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const AdapterParams p) {
     __shared__ float part[kMaxR];
     __shared__ __align__(16) float v[kMaxR];
     cg::cluster_group cluster = cg::this_cluster();
@@ -666,7 +668,10 @@ int check_sizes(const spconv_adapter_args *a) {
         return SPCONV_ERR_INVALID_ARG;
     if (a->dtype < SPCONV_F32 || a->dtype > SPCONV_F16) return SPCONV_ERR_INVALID_ARG;
     if (!stride_ok(a->x_stride_n) || !stride_ok(a->x_stride_c)) return SPCONV_ERR_INVALID_ARG;
-    return a->R > kMaxR ? SPCONV_ERR_UNSUPPORTED : SPCONV_OK;
+    constexpr int kMost = 1 << 26;  // rows, channels, positions: their products with a tile's
+                                    // pieces stay within 32 bits
+    return a->R > kMaxR || a->C > kMost || a->M > kMost || a->P > kMost ? SPCONV_ERR_UNSUPPORTED
+                                                                       : SPCONV_OK;
 }
 
 // Launches `jobs` clusters of `ranks` blocks.
@@ -706,11 +711,6 @@ int ranks_for(const AdapterParams &p, int64_t jobs, int64_t want, int least) {
 }  // namespace spconv
 
 using namespace spconv::seq;
-
-SPCONV_API int64_t spconv_adapter_workspace(const spconv_adapter_args *a) {
-    (void)a;
-    return 0;
-}
 
 SPCONV_API int spconv_adapter_add(const spconv_adapter_args *a, void *stream) {
     const int st = check_sizes(a);

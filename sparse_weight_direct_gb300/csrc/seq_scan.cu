@@ -583,8 +583,6 @@ bool elements(size_t e, std::initializer_list<const void *> ps) {
 
 namespace {
 
-constexpr int64_t kSplitBelow = kSMs, kSplitTo = 4 * kSMs;  // blocks
-
 // f(SPT, LPC) for the smallest tile of a step that holds S states.
 template <typename F>
 int by_lanes(int S, F f) {
@@ -598,20 +596,33 @@ int by_lanes(int S, F f) {
 
 // Blocks and chunks of the forward scan.  One pass over a sequence needs a block
 // per 32 channels of each sequence; where that leaves SMs idle the sequence is
-// cut, into chunks of 128 positions at least.  Two more passes over the states
-// are the price: what every chunk leaves from zero (no outputs), and the join.
+// cut.  The price are two more passes over the states: what every chunk leaves
+// from zero (without outputs it takes two thirds of a pass) and the join.
+// The time of a plan, in positions of a full GPU: four blocks fit an SM, and
+// one takes 0.62 of what it takes among four, two 0.73 (measured: 4096
+// channels x 2048 positions of 2, 3 and 4 sequences take 166, 185 and 205 us).
+// One sequence of those: 4 chunks (512 blocks, one wave) take 93 us, 5 (640) took
+// 131; two sequences whole take 166, in 3 chunks each they took 222.
 void plan_chunks(ScanParams &p) {
     p.blocks_per_group = (p.per_group + 31) / 32;
     const int64_t blocks = (int64_t)p.groups * p.blocks_per_group * p.N;
-    const int64_t most = p.L / 128;
+    auto time = [&](int64_t chunks, int64_t len) {
+        const int64_t all = blocks * chunks, wave = 4 * kSMs, rest = all % wave;
+        const double last = rest ? 0.62 + 0.11 * (double)((rest + kSMs - 1) / kSMs) : 0.;
+        return ((double)(all / wave) * 1.06 + last) * (double)len;
+    };
     p.chunks = 1;
     p.chunk_len = p.L;
-    if (blocks >= kSplitBelow || most < 2) return;
-    int64_t want = (kSplitTo + blocks - 1) / blocks;
-    if (want > most) want = most;
-    const int64_t len = ((p.L + want - 1) / want + 31) / 32 * 32;  // whole tiles of either type
-    p.chunk_len = (int)len;
-    p.chunks = (int)((p.L + len - 1) / len);
+    double best = time(1, p.L);
+    for (int64_t k = 2; k <= p.L / 64 && (k - 1) * blocks < 4 * kSMs; ++k) {
+        const int64_t len = ((p.L + k - 1) / k + 31) / 32 * 32;  // whole tiles of either type
+        const int64_t chunks = (p.L + len - 1) / len;
+        const double t = 1.65 * time(chunks, len) + 80.;
+        if (t >= best) continue;
+        best = t;
+        p.chunk_len = (int)len;
+        p.chunks = (int)chunks;
+    }
 }
 
 int64_t state_floats(const ScanParams &p) {

@@ -33,9 +33,9 @@ _torch = None
 
 def _load():
     """torch and its types, on the first call (the package itself loads without)."""
-    global _torch, _Tensor, _codes, _f32, _i32, _empty, _raw_stream, _current_device, _library
+    global _torch, _Tensor, _codes, _f32, _i32, _empty, _empty_like, _raw_stream, _current_device, _library
     import torch
-    _Tensor, _empty = torch.Tensor, torch.empty
+    _Tensor, _empty, _empty_like = torch.Tensor, torch.empty, torch.empty_like
     _f32, _i32 = torch.float32, torch.int32
     _codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -85,6 +85,11 @@ def _new(shape, dtype, device):
     return _empty(shape, dtype=dtype, device=device)
 
 
+def _like(t):
+    """A new contiguous tensor of t's shape and type."""
+    return _empty_like(t) if t.is_contiguous() else _empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _dims(t, count, name):
     if not isinstance(t, _Tensor) or t.dim() != count:
         _fail(f"{name} must be a tensor with {count} dimensions")
@@ -98,11 +103,11 @@ def _run(function, args, device, stream, tensors, query=None):
     current = _raw_stream(device)
     ptr = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
     workspace = None
-    if query is not None and (need := query(args + _no_workspace)):
-        workspace = _empty(need, dtype=_torch.uint8, device=device)
-        args += _pack_workspace(workspace.data_ptr(), need)
-    else:
-        args += _no_workspace
+    if query is not None:
+        need = query(args + _no_workspace)
+        if need:
+            workspace = _empty(need, dtype=_torch.uint8, device=device)
+        args += _pack_workspace(workspace.data_ptr(), need) if need else _no_workspace
     rc = function(args, ptr)
     if rc:
         _lib.check(rc, function.__name__)
@@ -128,14 +133,14 @@ def short_conv(x, weight, bias=None, *, silu: bool = True, state=None, final_sta
     K = _dims(weight, 2, "weight")[1]
     st = (N, C, K - 1)
     if out is None:
-        out = _new(shape, dt, dev)
+        out = _like(x)
     args = _pack_conv(
         N, C, L, K, code, silu, 0, 0, x.stride(0), x.stride(1), 0, 0,
         _rows(x, "x", dt, dev, shape), _whole(weight, "weight", _f32, dev, (C, K)),
         _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
         _whole(lengths, "lengths", _i32, dev, (N,)), 0, _whole(out, "out", dt, dev, shape),
         _whole(final_state, "final_state", dt, dev, st), 0, 0, 0, 0, 0, 0, 0)
-    _run(_library.spconv_short_conv, args, dev, stream,
+    _run(_library.spconv_short_conv, args + _no_workspace, dev, stream,
          (x, weight, bias, state, lengths, out, final_state))
     return out
 
@@ -177,13 +182,14 @@ def short_conv_step(x, state, weight, bias=None, *, silu: bool = True, slots=Non
     K = _dims(weight, 2, "weight")[1]
     pool = _dims(state, 3, "state")[0]
     if out is None:
-        out = _new(shape, dt, dev)
+        out = _like(x)
     args = _pack_conv(
         N, C, 1, K, code, silu, pool, 0, x.stride(0), 1, 0, 0, _rows(x, "x", dt, dev, shape),
         _whole(weight, "weight", _f32, dev, (C, K)), _whole(bias, "bias", _f32, dev, (C,)), 0, 0,
         _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape), 0,
         _whole(state, "state", dt, dev, (pool, C, K - 1)), 0, 0, 0, 0, 0, 0)
-    _run(_library.spconv_short_conv_step, args, dev, stream, (x, weight, bias, slots, out, state))
+    _run(_library.spconv_short_conv_step, args + _no_workspace, dev, stream,
+         (x, weight, bias, slots, out, state))
     return out
 
 
@@ -233,7 +239,7 @@ def scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool =
     given, S = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0)
     states = (shape[0], shape[1], S)
     if out is None:
-        out = _new(shape, dt, dev)
+        out = _like(u)
     args = _pack_scan(
         *given, _whole(state, "state", _f32, dev, states),
         _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, _whole(out, "out", dt, dev, shape),
@@ -284,11 +290,11 @@ def scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, soft
     pool = _dims(state, 3, "state")[0]
     given, S = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, True, pool)
     if out is None:
-        out = _new(shape, dt, dev)
+        out = _like(u)
     args = _pack_scan(
         *given, 0, 0, _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape),
         0, _whole(state, "state", _f32, dev, (pool, ch, S)), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    _run(_library.spconv_scan_step, args, dev, stream,
+    _run(_library.spconv_scan_step, args + _no_workspace, dev, stream,
          (u, delta, A, B, C, D, z, delta_bias, slots, out, state))
     return out
 
@@ -311,12 +317,11 @@ def adapter_add(y, x, a, b, index, *, scale=None, out=None, stream=None):
         _fail("y must be given")
     y_at = _whole(y, "y", dt, dev, shape)
     if out is None:
-        out = _new(shape, dt, dev)
+        out = _like(y)
     args = _pack_adapter(
         N, P, C, M, R, K, code, 0, x.stride(0), x.stride(1), _rows(x, "x", dt, dev, x.shape),
         _whole(a, "a", dt, dev, (K, R, C)), _whole(b, "b", dt, dev, (K, M, R)),
         _whole(index, "index", _i32, dev, (N,)), _whole(scale, "scale", _f32, dev, (K,)), y_at,
         _whole(out, "out", dt, dev, shape))
-    _run(_library.spconv_adapter_add, args, dev, stream, (y, x, a, b, index, scale, out),
-         _library.spconv_adapter_workspace)
+    _run(_library.spconv_adapter_add, args, dev, stream, (y, x, a, b, index, scale, out))
     return out

@@ -540,9 +540,8 @@ def scan_args(**change):
 def adapter_args(**change):
     a = AdapterArgs(2, 5, 4, 6, 8, 3, 0)
     a.x_stride_n, a.x_stride_c = 20, 5
-    for i, n in enumerate("x a b index scale y out workspace".split()):
+    for i, n in enumerate("x a b index scale y out".split()):
         setattr(a, n, GOOD + 0x10000 * i)
-    a.workspace_bytes = 1 << 16
     for k, v in change.items():
         setattr(a, k, v)
     return a
@@ -560,7 +559,8 @@ REFUSED = [
      (dict(N=4096, L=4096, workspace_bytes=0), BAD), (dict(N=4096, L=4096, workspace=None), BAD)]),
     ("spconv_short_conv_step", conv_args, [(dict(num_slots=1), BAD), (dict(num_slots=2, x_stride_c=5), BAD),
      (dict(num_slots=2, x_stride_c=1, pool=None), BAD), (dict(num_slots=2, x_stride_c=1, x=None), BAD),
-     (dict(num_slots=-1, x_stride_c=1), BAD), (dict(num_slots=2, x_stride_c=1, K=6), BEYOND)]),
+     (dict(num_slots=-1, x_stride_c=1), BAD), (dict(num_slots=2, x_stride_c=1, K=6), BEYOND),
+     (dict(N=70000, num_slots=70000, x_stride_c=1), BEYOND)]),
     ("spconv_scan", scan_args, [(dict(N=-1), BAD), (dict(S=0), BAD), (dict(S=65), BEYOND), (dict(groups=0), BAD),
      (dict(groups=3), BAD), (dict(dtype=7), BAD), (dict(softplus=2), BAD), (dict(u=None), BAD), (dict(A=None), BAD),
      (dict(B=None), BAD), (dict(y=None), BAD), (dict(y=GOOD), BAD), (dict(u=GOOD + 2), BAD), (dict(A=GOOD + 1), BAD),
@@ -571,8 +571,10 @@ REFUSED = [
      (dict(workspace=GOOD + 4), BAD), (dict(S=65), BEYOND), (dict(N=70000, workspace_bytes=1 << 40), BEYOND)]),
     ("spconv_scan_step", scan_args, [(dict(num_slots=1), BAD), (dict(num_slots=2), BAD),
      (dict(num_slots=2, u_stride_c=1, delta_stride_c=1, z_stride_c=1, b_stride_s=1, c_stride_s=1, pool=None), BAD),
-     (dict(num_slots=2, u_stride_c=1, delta_stride_c=1, z_stride_c=1, b_stride_s=1, c_stride_s=1, y=GOOD), BAD)]),
+     (dict(num_slots=2, u_stride_c=1, delta_stride_c=1, z_stride_c=1, b_stride_s=1, c_stride_s=1, y=GOOD), BAD),
+     (dict(N=70000), BEYOND)]),
     ("spconv_adapter_add", adapter_args, [(dict(N=-1), BAD), (dict(R=0), BAD), (dict(R=65), BEYOND),
+     (dict(P=1 << 27), BEYOND), (dict(M=1 << 27), BEYOND), (dict(C=1 << 27), BEYOND),
      (dict(adapters=-1), BAD), (dict(dtype=3), BAD), (dict(x=None), BAD), (dict(a=None), BAD), (dict(b=None), BAD),
      (dict(index=None), BAD), (dict(y=None), BAD), (dict(out=None), BAD), (dict(out=GOOD), BAD),
      (dict(out=GOOD + 0x50000 + 4), BAD), (dict(x=GOOD + 2), BAD), (dict(x_stride_n=-1), BAD),
