@@ -527,35 +527,38 @@ __global__ void __launch_bounds__(kBackThreads) gradient_kernel(const ScanParams
     }
 }
 
-// dA, dD and ddelta_bias: the segments' shares in their order.
-__global__ void __launch_bounds__(256) join_weights_kernel(const ScanParams p) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t per = (int64_t)p.channels * (p.S + 2);
-    if (i >= per) return;
-    float v = 0.f;
-    for (int64_t k = 0; k < (int64_t)p.N * p.segments; ++k) v += p.part_a[k * per + i];
-    const int64_t c = i / (p.S + 2);
-    const int s = (int)(i - c * (p.S + 2));
-    if (s < p.S)
-        p.dA[c * p.S + s] = v;
-    else if (s == p.S) {
-        if (p.dD) p.dD[c] = v;
-    } else if (p.ddelta_bias) {
-        p.ddelta_bias[c] = v;
-    }
-}
-
-// dB and dC: the blocks' shares in their order, [position][state] to
-// [state][position].
+// Joins the blocks' shares in their order.  The first `weight_blocks` blocks take
+// dA, dD and ddelta_bias, the shares of segments; the others dB and dC, the
+// shares of blocks, [position][state] to [state][position].
 template <typename T>
-__global__ void __launch_bounds__(256) join_bc_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(256) join_shares_kernel(const ScanParams p, int weight_blocks) {
+    if ((int)blockIdx.x < weight_blocks) {
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        const int64_t per = (int64_t)p.channels * (p.S + 2);
+        if (i >= per) return;
+        float v = 0.f;
+        const int64_t count = (int64_t)p.N * p.segments;
+#pragma unroll 4
+        for (int64_t k = 0; k < count; ++k) v += p.part_a[k * per + i];
+        const int64_t c = i / (p.S + 2);
+        const int s = (int)(i - c * (p.S + 2));
+        if (s < p.S)
+            p.dA[c * p.S + s] = v;
+        else if (s == p.S) {
+            if (p.dD) p.dD[c] = v;
+        } else if (p.ddelta_bias) {
+            p.ddelta_bias[c] = v;
+        }
+        return;
+    }
     const int64_t per = (int64_t)p.N * p.L * p.S;  // of one block and matrix
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (int64_t)(blockIdx.x - weight_blocks) * 256 + threadIdx.x;
     const int blocks = p.groups * p.blocks_per_group;
     if (i >= 2 * p.groups * per) return;
     const int64_t k = i / per, r = i - k * per;
     const int which = (int)(k / p.groups), g = (int)(k - which * p.groups);
     float v = 0.f;
+#pragma unroll 4
     for (int b = 0; b < p.blocks_per_group; ++b)
         v += p.part_bc[((int64_t)which * blocks + g * p.blocks_per_group + b) * per + r];
     const int64_t nt = r / p.S, n = nt / p.L, t = nt - n * p.L;
@@ -679,7 +682,7 @@ SPCONV_API int spconv_scan_backward(const spconv_scan_args *a, void *stream) {
     p.vec_y = rows_aligned(a->du, 0, L, e) && rows_aligned(a->ddelta, 0, L, e) &&
               (!a->dz || rows_aligned(a->dz, 0, L, e));
     const int64_t weights = (int64_t)p.channels * (p.S + 2), bc = 2LL * p.groups * p.N * L * p.S;
-    if (p.segments > 65535 || (bc + 255) / 256 > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
+    if (p.segments > 65535 || (weights + bc + 511) / 256 > 0x7fffffff) return SPCONV_ERR_UNSUPPORTED;
     return by_dtype(a->dtype, [&](auto t) {
         return by_states(a->S, [&](auto k) {
             using T = decltype(t);
@@ -696,8 +699,8 @@ SPCONV_API int spconv_scan_backward(const spconv_scan_args *a, void *stream) {
             if (int rc = scan_join_chunks(p, true, s)) return rc;
             grad<<<grid, kBackThreads, G::kAll * 4, s>>>(p);
             if (int rc = launch_status()) return rc;
-            join_weights_kernel<<<(unsigned)((weights + 255) / 256), 256, 0, s>>>(p);
-            join_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(p);
+            const int64_t first = (weights + 255) / 256;
+            join_shares_kernel<T><<<(unsigned)(first + (bc + 255) / 256), 256, 0, s>>>(p, (int)first);
             return launch_status();
         });
     });

@@ -62,12 +62,13 @@ def _begin(t, name, dims):
 
 
 def _rows(t, name, dtype, device, shape):
-    """Pointer to an activation whose last dimension is contiguous (its other strides are free)."""
+    """Pointer to and strides of an activation whose last dimension is contiguous."""
     if not isinstance(t, _Tensor) or t.dtype != dtype or t.get_device() != device or t.shape != shape:
         _fail(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on CUDA device {device}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         _fail(f"{name} must be contiguous along its last dimension")
-    return t.data_ptr()
+    return t.data_ptr(), strides
 
 
 def _whole(t, name, dtype, device, shape):
@@ -132,11 +133,11 @@ def short_conv(x, weight, bias=None, *, silu: bool = True, state=None, final_sta
     shape = N, C, L = x.shape
     K = _dims(weight, 2, "weight")[1]
     st = (N, C, K - 1)
+    x_at, (xn, xc, _) = _rows(x, "x", dt, dev, shape)
     if out is None:
         out = _like(x)
     args = _pack_conv(
-        N, C, L, K, code, silu, 0, 0, x.stride(0), x.stride(1), 0, 0,
-        _rows(x, "x", dt, dev, shape), _whole(weight, "weight", _f32, dev, (C, K)),
+        N, C, L, K, code, silu, 0, 0, xn, xc, 0, 0, x_at, _whole(weight, "weight", _f32, dev, (C, K)),
         _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
         _whole(lengths, "lengths", _i32, dev, (N,)), 0, _whole(out, "out", dt, dev, shape),
         _whole(final_state, "final_state", dt, dev, st), 0, 0, 0, 0, 0, 0, 0)
@@ -154,13 +155,13 @@ def short_conv_backward(dy, x, weight, bias=None, *, silu: bool = True, state=No
     shape = N, C, L = x.shape
     K = _dims(weight, 2, "weight")[1]
     st = (N, C, K - 1)
-    dy_at = _rows(dy, "dy", dt, dev, shape)
+    x_at, (xn, xc, _) = _rows(x, "x", dt, dev, shape)
+    dy_at, (dyn, dyc, _) = _rows(dy, "dy", dt, dev, shape)
     dx, dw = _new(shape, dt, dev), _new((C, K), _f32, dev)
     db = _new((C,), _f32, dev) if bias is not None else None
     ds = _new(st, dt, dev) if state is not None else None
     args = _pack_conv(
-        N, C, L, K, code, silu, 0, 0, x.stride(0), x.stride(1), dy.stride(0), dy.stride(1),
-        _rows(x, "x", dt, dev, shape), _whole(weight, "weight", _f32, dev, (C, K)),
+        N, C, L, K, code, silu, 0, 0, xn, xc, dyn, dyc, x_at, _whole(weight, "weight", _f32, dev, (C, K)),
         _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
         _whole(lengths, "lengths", _i32, dev, (N,)), 0, 0, 0, 0, dy_at,
         _whole(dfinal_state, "dfinal_state", dt, dev, st), dx.data_ptr(),
@@ -181,11 +182,11 @@ def short_conv_step(x, state, weight, bias=None, *, silu: bool = True, slots=Non
     shape = N, C = x.shape
     K = _dims(weight, 2, "weight")[1]
     pool = _dims(state, 3, "state")[0]
+    x_at, (xn, _) = _rows(x, "x", dt, dev, shape)
     if out is None:
         out = _like(x)
     args = _pack_conv(
-        N, C, 1, K, code, silu, pool, 0, x.stride(0), 1, 0, 0, _rows(x, "x", dt, dev, shape),
-        _whole(weight, "weight", _f32, dev, (C, K)), _whole(bias, "bias", _f32, dev, (C,)), 0, 0,
+        N, C, 1, K, code, silu, pool, 0, xn, 1, 0, 0, x_at, _whole(weight, "weight", _f32, dev, (C, K)), _whole(bias, "bias", _f32, dev, (C,)), 0, 0,
         _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape), 0,
         _whole(state, "state", dt, dev, (pool, C, K - 1)), 0, 0, 0, 0, 0, 0)
     _run(_library.spconv_short_conv_step, args + _no_workspace, dev, stream,
@@ -194,32 +195,38 @@ def short_conv_step(x, state, weight, bias=None, *, silu: bool = True, slots=Non
 
 
 def _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, step, pool, dy=None):
-    """What the scan's calls have in common, up to the pointer to delta_bias, and S.
+    """What the scan's calls have in common, up to the pointer to delta_bias, S, and the pointer to dy.
     B and C: (N, S[, L]) or (N, groups, S[, L])."""
     shape = u.shape
     N, ch = shape[0], shape[1]
     L = 1 if step else shape[2]
     S = _dims(A, 2, "A")[1]
-    tail = (S,) if step else (S, L)
-    both, strides, G = [], [], 1
-    for t, name in ((B, "B"), (C, "C")):
-        grouped = isinstance(t, _Tensor) and t.dim() == 2 + len(tail)
-        if grouped and name == "B":
-            G = t.shape[1]
-            if G < 1 or ch % G:
-                _fail("the groups of B and C must divide the channels")
-        both.append(_rows(t, name, dt, dev, (N, G) + tail if grouped else (N,) + tail))
-        strides += (t.stride(0), t.stride(1) if grouped else 0, 1 if step else t.stride(-2))
-    if G > 1 and not grouped:
+    dims = 3 if step else 4  # of grouped B and C
+    G = 1
+    if isinstance(B, _Tensor) and B.dim() == dims:
+        G = B.shape[1]
+        if G < 1 or ch % G:
+            _fail("the groups of B and C must divide the channels")
+    whole, plain = ((N, G, S), (N, S)) if step else ((N, G, S, L), (N, S, L))
+    grouped_b = isinstance(B, _Tensor) and B.dim() == dims
+    grouped_c = isinstance(C, _Tensor) and C.dim() == dims
+    if G > 1 and not grouped_c:
         _fail("B and C must have the same groups")
-    own = [_rows(u, "u", dt, dev, shape), _rows(delta, "delta", dt, dev, shape),
-           0 if z is None else _rows(z, "z", dt, dev, shape)]
-    rows = []
-    for t in (u, delta, z, dy):
-        rows += (0, 0) if t is None else (t.stride(0), 1 if step else t.stride(1))
-    return (N, ch, L, S, G, code, softplus, pool, *rows, *strides, *own, *both,
+    at_b, sb = _rows(B, "B", dt, dev, whole if grouped_b else plain)
+    at_c, sc = _rows(C, "C", dt, dev, whole if grouped_c else plain)
+    at_u, su = _rows(u, "u", dt, dev, shape)
+    at_d, sd = _rows(delta, "delta", dt, dev, shape)
+    at_z, sz = (0, (0, 0)) if z is None else _rows(z, "z", dt, dev, shape)
+    at_dy, sy = (0, (0, 0)) if dy is None else _rows(dy, "dy", dt, dev, shape)
+    bg, cg = sb[1] if grouped_b else 0, sc[1] if grouped_c else 0
+    if step:
+        strides = (su[0], 1, sd[0], 1, sz[0], 1, 0, 0, sb[0], bg, 1, sc[0], cg, 1)
+    else:
+        strides = (su[0], su[1], sd[0], sd[1], sz[0], sz[1], sy[0], sy[1], sb[0], bg, sb[-2], sc[0], cg,
+                   sc[-2])
+    return (N, ch, L, S, G, code, softplus, pool, *strides, at_u, at_d, at_z, at_b, at_c,
             _whole(A, "A", _f32, dev, (ch, S)), _whole(D, "D", _f32, dev, (ch,)),
-            _whole(delta_bias, "delta_bias", _f32, dev, (ch,))), S
+            _whole(delta_bias, "delta_bias", _f32, dev, (ch,))), S, at_dy
 
 
 def scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool = True, state=None,
@@ -236,7 +243,7 @@ def scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool =
     overwritten with h behind the last position.  Returns y."""
     dt, code, dev = _begin(u, "u", 3)
     shape = u.shape
-    given, S = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0)
+    given, S, _ = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0)
     states = (shape[0], shape[1], S)
     if out is None:
         out = _like(u)
@@ -257,9 +264,10 @@ def scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, sof
     ddelta_bias and dstate, None for an argument that was not given."""
     dt, code, dev = _begin(u, "u", 3)
     shape = u.shape
-    dy_at = _rows(dy, "dy", dt, dev, shape)
-    given, S = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0,
-                            dy)
+    if dy is None:
+        _fail("dy must be given")
+    given, S, dy_at = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus,
+                                   False, 0, dy)
     states = (shape[0], shape[1], S)
     g = dict(du=_new(shape, dt, dev), ddelta=_new(shape, dt, dev), dA=_new(A.shape, _f32, dev),
              dB=_new(B.shape, dt, dev), dC=_new(C.shape, dt, dev),
@@ -288,7 +296,7 @@ def scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, soft
     dt, code, dev = _begin(u, "u", 2)
     shape = N, ch = u.shape
     pool = _dims(state, 3, "state")[0]
-    given, S = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, True, pool)
+    given, S, _ = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, True, pool)
     if out is None:
         out = _like(u)
     args = _pack_scan(
@@ -316,11 +324,11 @@ def adapter_add(y, x, a, b, index, *, scale=None, out=None, stream=None):
     if y is None:
         _fail("y must be given")
     y_at = _whole(y, "y", dt, dev, shape)
+    x_at, xs = _rows(x, "x", dt, dev, x.shape)
     if out is None:
         out = _like(y)
     args = _pack_adapter(
-        N, P, C, M, R, K, code, 0, x.stride(0), x.stride(1), _rows(x, "x", dt, dev, x.shape),
-        _whole(a, "a", dt, dev, (K, R, C)), _whole(b, "b", dt, dev, (K, M, R)),
+        N, P, C, M, R, K, code, 0, xs[0], xs[1], x_at, _whole(a, "a", dt, dev, (K, R, C)), _whole(b, "b", dt, dev, (K, M, R)),
         _whole(index, "index", _i32, dev, (N,)), _whole(scale, "scale", _f32, dev, (K,)), y_at,
         _whole(out, "out", dt, dev, shape))
     _run(_library.spconv_adapter_add, args, dev, stream, (y, x, a, b, index, scale, out))
