@@ -415,10 +415,11 @@ __global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, in
 // Step: LPC lanes per request and channel, each with SPT of its states, which
 // are read and written once.  Bound by that traffic, so by how much of it is
 // under way: a thread takes one request after the other for its channel, with
-// the next one's states and inputs being read, and its row of A once.  (One
-// request per thread, 128 x 4096 x 16 in bf16: 28 us.)
+// the next one's states and inputs being read, and its row of A once.  128 x
+// 4096 x 16 in bf16: one request per thread 28 us, two blocks per SM 24, three
+// (B and C kept as words) 18, four spill and take 20.
 template <typename T, int SPT, int LPC>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(256, SPT <= 8 ? 3 : 1) scan_step_kernel(const ScanParams p) {
     const int64_t c64 = (int64_t)blockIdx.x * (256 / LPC) + threadIdx.x / LPC;
     // lane j holds states s0 .. s0 + SPT-1; of whole rows, fours of them LPC
     // fours apart, so that a warp's reads and writes are contiguous
@@ -437,9 +438,12 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
     for (int k = 0; k < SPT; ++k) A[k] = place(k) < p.S ? rowA[place(k)] : 0.f;
 #pragma unroll
     for (int k = 0; k < SPT; ++k) A[k] *= kLog2e;
+    constexpr int kFours = SPT % 4 == 0 ? SPT / 4 : 1;
     struct Inputs {
         float *row;  // the request's states, nullptr without
-        float h[SPT], b[SPT], c[SPT], u, d, z;
+        float h[SPT];
+        T u, d, z;
+        Run<T, 4> b[kFours], c[kFours];  // of whole rows (as words: registers are blocks)
     } next;
     auto fetch = [&](int n) {
         next.row = nullptr;
@@ -447,34 +451,23 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
         const int slot = p.slots ? p.slots[n] : n;
         if (slot < 0 || slot >= p.num_slots) return;
         next.row = p.pool + ((int64_t)slot * p.channels + c) * p.S;
-        next.u = to_f32(u[n * p.u_sn]);
-        next.d = to_f32(d[n * p.d_sn]);
-        if (p.z) next.z = to_f32(z[n * p.z_sn]);
-        const T *Bn = B + n * p.b_sn, *Cn = C + n * p.c_sn;
+        next.u = u[n * p.u_sn];
+        next.d = d[n * p.d_sn];
+        if (p.z) next.z = z[n * p.z_sn];
         if constexpr (SPT % 4 == 0) {
             if (whole) {
+                const T *Bn = B + n * p.b_sn, *Cn = C + n * p.c_sn;
 #pragma unroll
                 for (int k = 0; k < SPT; k += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(next.row + place(k));
                     next.h[k] = f.x; next.h[k + 1] = f.y; next.h[k + 2] = f.z; next.h[k + 3] = f.w;
-                    Run<T, 4> rb, rc;
-                    load_run(rb, Bn, place(k), p.S, true);
-                    load_run(rc, Cn, place(k), p.S, true);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        next.b[k + i] = rb[i];
-                        next.c[k + i] = rc[i];
-                    }
+                    load_run(next.b[k / 4], Bn, place(k), p.S, true);
+                    load_run(next.c[k / 4], Cn, place(k), p.S, true);
                 }
                 return;
             }
         }
         load_states<SPT>(next.h, next.row, s0, p.S);
-#pragma unroll
-        for (int k = 0; k < SPT; ++k) {
-            next.b[k] = s0 + k < p.S ? to_f32(Bn[s0 + k]) : 0.f;
-            next.c[k] = s0 + k < p.S ? to_f32(Cn[s0 + k]) : 0.f;
-        }
     };
     fetch(blockIdx.y);
     for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
@@ -482,19 +475,28 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
         fetch(n + gridDim.y);
         float o = 0.f;
         if (now.row) {
-            const float raw = now.d + bias, dt = p.softplus ? softplus(raw) : raw;
-            const float du = dt * now.u;
-#pragma unroll
-            for (int k = 0; k < SPT; ++k) {
-                now.h[k] = fmaf(decay(dt, A[k]), now.h[k], du * now.b[k]);
-                o = fmaf(now.h[k], now.c[k], o);
-            }
+            const float raw = to_f32(now.d) + bias, dt = p.softplus ? softplus(raw) : raw;
+            const float du = dt * to_f32(now.u);
             if constexpr (SPT % 4 == 0) {
                 if (whole) {
+#pragma unroll
+                    for (int k = 0; k < SPT; ++k) {
+                        now.h[k] = fmaf(decay(dt, A[k]), now.h[k], du * now.b[k / 4][k % 4]);
+                        o = fmaf(now.h[k], now.c[k / 4][k % 4], o);
+                    }
 #pragma unroll
                     for (int k = 0; k < SPT; k += 4)
                         *reinterpret_cast<float4 *>(now.row + place(k)) =
                             make_float4(now.h[k], now.h[k + 1], now.h[k + 2], now.h[k + 3]);
+                }
+            }
+            if (!whole) {
+                const T *Bn = B + n * p.b_sn, *Cn = C + n * p.c_sn;
+#pragma unroll
+                for (int k = 0; k < SPT; ++k) {
+                    const bool in = s0 + k < p.S;
+                    now.h[k] = fmaf(decay(dt, A[k]), now.h[k], du * (in ? to_f32(Bn[s0 + k]) : 0.f));
+                    o = fmaf(now.h[k], in ? to_f32(Cn[s0 + k]) : 0.f, o);
                 }
             }
             if (!whole) store_states<SPT>(now.row, now.h, s0, p.S);
@@ -503,8 +505,8 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanParams p) {
         if (LPC == 4) o += __shfl_xor_sync(~0u, o, 2);
         if (on && j == 0) {
             if (now.row) {
-                o = fmaf(D, now.u, o);
-                if (p.z) o *= silu(now.z);
+                o = fmaf(D, to_f32(now.u), o);
+                if (p.z) o *= silu(to_f32(now.z));
             }
             static_cast<T *>(p.y)[(int64_t)n * p.channels + c] = from_f32<T>(o);
         }
@@ -728,7 +730,7 @@ SPCONV_API int spconv_scan_step(const spconv_scan_args *a, void *stream) {
         return by_lanes(a->S, [&](auto spt, auto lpc) {
             constexpr int SPT = decltype(spt)::value, LPC = decltype(lpc)::value, CB = 256 / LPC;
             const int64_t blocks = ((int64_t)a->channels + CB - 1) / CB;
-            int64_t side = (4 * kSMs + blocks - 1) / blocks;  // requests side by side: 4 blocks per SM
+            int64_t side = (6 * kSMs + blocks - 1) / blocks;  // requests side by side: 6 blocks per SM
             if (side > a->N) side = a->N;
             scan_step_kernel<decltype(t), SPT, LPC>
                 <<<dim3((unsigned)blocks, (unsigned)side), 256, 0,
