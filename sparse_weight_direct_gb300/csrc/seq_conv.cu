@@ -81,9 +81,56 @@ static __device__ __forceinline__ void load_behind(float *s, const T *row, int t
 // sequence after the other, the next one's inputs on their way; blocks x go
 // over the tiles of a row and the channels, y over the sequences.  Its
 // instructions are as near a bound as its bytes: a thread per run spent two
-// thirds of them on its place and its weights (82 us on 8 x 4096 x 2048 in bf16).
+// thirds of them on its place and its weights (82 us on 8 x 4096 x 2048 in
+// bf16), one loop for every case many on the cases (65 us).  So whole, aligned
+// runs of full sequences have a loop of their own (55 us, six blocks per SM).
+template <typename T, int K, bool SILU>
+static __device__ __forceinline__ void conv_whole_runs(const ConvParams &p, const float (&w)[K],
+                                                       float b, int c, int t0) {
+    const int64_t x_step = gridDim.y * p.x_sn, row_step = (int64_t)gridDim.y * p.C;
+    const T *x = static_cast<const T *>(p.x) + blockIdx.y * p.x_sn + c * p.x_sc + t0;
+    const int64_t row = (int64_t)blockIdx.y * p.C + c;
+    T *y = static_cast<T *>(p.y) + row * p.L + t0;
+    const T *state = p.state ? static_cast<const T *>(p.state) + row * (K - 1) : nullptr;
+    const int64_t y_step = row_step * p.L;
+    Run<T> in, left;
+    auto fetch = [&](int n) {
+        if (n >= p.N) return;
+        load_run(in, x, 0, kVec, true);
+        if (K > 1 && t0 > 0) {
+            load_run(left, x - kVec, 0, kVec, true);
+        } else if (K > 1) {
+            float f[kVec] = {};
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) f[kVec - (K - 1) + j] = state ? to_f32(state[j]) : 0.f;
+            left.put(f);
+        }
+        x += x_step;
+        if (state) state += row_step * (K - 1);
+    };
+    fetch(blockIdx.y);
+    for (int n = blockIdx.y; n < p.N; n += gridDim.y, y += y_step) {
+        float s[kVec + K - 1], o[kVec];
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) s[i] = left[kVec - (K - 1) + i];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) s[K - 1 + i] = in[i];
+        fetch(n + gridDim.y);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            o[i] = b;
+#pragma unroll
+            for (int k = 0; k < K; ++k) o[i] = fmaf(w[k], s[i + k], o[i]);
+            if (SILU) o[i] = silu(o[i]);
+        }
+        Run<T> out;
+        out.put(o);
+        *reinterpret_cast<Run<T> *>(y) = out;
+    }
+}
+
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4) conv_kernel(const ConvParams p) {
     const unsigned cb = blockIdx.x / (unsigned)p.tiles;
     const int tile = (int)(blockIdx.x - cb * p.tiles);
     const int lane = threadIdx.x & (p.tx - 1);
@@ -94,6 +141,21 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvParams p) {
 #pragma unroll
     for (int k = 0; k < K; ++k) w[k] = p.weight[(int64_t)c * K + k];
     const float b = p.bias ? p.bias[c] : 0.f;
+    if (p.vec_x && p.vec_y && !p.lengths && t0 + kVec <= p.L) {
+        if (p.silu)
+            conv_whole_runs<T, K, true>(p, w, b, c, t0);
+        else
+            conv_whole_runs<T, K, false>(p, w, b, c, t0);
+        if (K > 1 && p.final_state && run == 0) {  // (whole runs: L >= K - 1)
+            for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
+                const T *last = static_cast<const T *>(p.x) + n * p.x_sn + c * p.x_sc + p.L - (K - 1);
+                T *fin = static_cast<T *>(p.final_state) + ((int64_t)n * p.C + c) * (K - 1);
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) fin[j] = last[j];
+            }
+        }
+        return;
+    }
     const int64_t x_step = gridDim.y * p.x_sn, row_step = (int64_t)gridDim.y * p.C;
     const T *x = static_cast<const T *>(p.x) + blockIdx.y * p.x_sn + c * p.x_sc;
     int64_t row = (int64_t)blockIdx.y * p.C + c;
