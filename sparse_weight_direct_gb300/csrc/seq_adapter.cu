@@ -34,6 +34,7 @@ struct AdapterParams {
     int64_t x_sn, x_sc;
     int N, P, C, M, R, adapters;
     int tiles;                     // prompts: tiles of positions of a request
+    int row_lanes;                 // tokens: lanes that share a row of b (a power of two)
     int vec_x, vec_a, vec_b, vec_y;  // rows can be read 16 (b of prompts: 4) bytes at a time
 };
 
@@ -550,12 +551,14 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
 constexpr int kTokenThreads = 256, kTokenWarps = kTokenThreads / 32;
 
 // A cluster per token.  A warp sums two rows of a at a time over the block's
-// channels, every block adds the ranks' parts of v, a thread sums rows of b.
+// channels, every block adds the ranks' parts of v, and row_lanes lanes sum a row
+// of b, 16 bytes each (with a lane per row a read takes 16 bytes of 32 lines).
 // What does not depend on v -- the first rows of b, of y -- is read before it.
-// Three blocks fit an SM: 48 tokens' 384 run at once (7.1 us; two an SM 8.9, four with
-// fewer registers 9.5; 4096 x 4096, rank 16, bf16).
+// What counts is how many reads are under way: 48 tokens, 4096 x 4096, rank 16,
+// bf16 take 6.0 us (two blocks per SM 9.2); 128 of rank 64 take 38 (three
+// blocks 49; four rows of a at a time in three blocks 43).
 template <typename T>
-__global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const AdapterParams p) {
+__global__ void __launch_bounds__(kTokenThreads, 4) token_kernel(const AdapterParams p) {
     __shared__ float part[kMaxR];
     __shared__ __align__(16) float v[kMaxR];
     cg::cluster_group cluster = cg::this_cluster();
@@ -575,25 +578,29 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const AdapterPa
     const T *a = static_cast<const T *>(p.a) + (int64_t)id * p.R * p.C;
     const T *b = static_cast<const T *>(p.b) + (int64_t)id * p.M * p.R;
     const float scale = p.scale ? p.scale[id] : 1.f;
-    constexpr int V = 16 / sizeof(T), kEarly = 2;
+    constexpr int V = 16 / sizeof(T), RW = 2, kRows = 4;  // kRows: of b that a lane has under way
     // channels in whole vectors, so that a block's slice starts on one
     const int vectors = (p.C + V - 1) / V;
     const int c_first = (int)((int64_t)vectors * rank / ranks) * V;
     const int c_last = min(p.C, (int)((int64_t)vectors * (rank + 1) / ranks) * V);
-    const int m0 = m_first + threadIdx.x;
-    Run<T, V> early[kEarly];
-    float y0 = 0.f;
+    const int part_of = threadIdx.x & (p.row_lanes - 1), side = kTokenThreads / p.row_lanes;
+    Run<T, V> rows[kRows];
+    float ys[kRows];
+    auto fetch = [&](int m) {
 #pragma unroll
-    for (int k = 0; k < kEarly; ++k)
-        load_run(early[k], b + (int64_t)m0 * p.R, k * V, m0 < m_last ? p.R : 0, p.vec_b);
-    if (m0 < m_last) y0 = to_f32(y[m0]);
-    for (int r0 = warp * 2; r0 < p.R; r0 += kTokenWarps * 2) {
-        float s[2] = {0.f, 0.f};
-        const bool two = r0 + 1 < p.R;
+        for (int k = 0; k < kRows; ++k, m += side) {
+            load_run(rows[k], b + (int64_t)m * p.R, part_of * V, m < m_last ? p.R : 0, p.vec_b);
+            ys[k] = part_of == 0 && m < m_last ? to_f32(y[m]) : 0.f;
+        }
+    };
+    int m = m_first + threadIdx.x / p.row_lanes;
+    fetch(m);
+    for (int r0 = warp * RW; r0 < p.R; r0 += kTokenWarps * RW) {
+        float s[RW] = {};
         const T *row = a + (int64_t)r0 * p.C;
 #pragma unroll 2
         for (int c = c_first + lane * V; c < c_last; c += 32 * V) {
-            Run<T, V> xr, ar, br;
+            Run<T, V> xr, ar[RW];
             if (p.x_sc == 1) {
                 load_run(xr, x, c, c_last, p.vec_x);
             } else {
@@ -602,22 +609,22 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const AdapterPa
                 for (int i = 0; i < V; ++i) f[i] = c + i < c_last ? to_f32(x[(c + i) * p.x_sc]) : 0.f;
                 xr.put(f);
             }
-            load_run(ar, row, c, c_last, p.vec_a);
-            load_run(br, row + p.C, c, two ? c_last : 0, p.vec_a);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                s[0] = fmaf(ar[i], xr[i], s[0]);
-                s[1] = fmaf(br[i], xr[i], s[1]);
-            }
+            for (int k = 0; k < RW; ++k)
+                load_run(ar[k], row + (int64_t)k * p.C, c, r0 + k < p.R ? c_last : 0, p.vec_a);
+#pragma unroll
+            for (int k = 0; k < RW; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[k] = fmaf(ar[k][i], xr[i], s[k]);
         }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            s[0] += __shfl_xor_sync(~0u, s[0], o);
-            s[1] += __shfl_xor_sync(~0u, s[1], o);
-        }
+        for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < RW; ++k) s[k] += __shfl_xor_sync(~0u, s[k], o);
         if (lane == 0) {
-            part[r0] = s[0];
-            if (two) part[r0 + 1] = s[1];
+#pragma unroll
+            for (int k = 0; k < RW; ++k)
+                if (r0 + k < p.R) part[r0 + k] = s[k];
         }
     }
     cluster.sync();
@@ -635,28 +642,28 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const AdapterPa
     }
     __syncthreads();
     auto left = cluster.barrier_arrive();  // this block has read the others' parts
-    for (int m = m0; m < m_last; m += kTokenThreads) {
-        const T *row = b + (int64_t)m * p.R;
-        float s = 0.f;
+    float mine[V];  // v against the lane's part of a row
 #pragma unroll
-        for (int k = 0; k < kMaxR / V; ++k) {
-            if (k * V >= p.R) break;
-            Run<T, V> br;
-            if (k < kEarly && m == m0)
-                br = early[k < kEarly ? k : 0];
-            else
-                load_run(br, row, k * V, p.R, p.vec_b);
-            // (behind R both are zero)
+    for (int i = 0; i < V; ++i) mine[i] = part_of * V + i < kMaxR ? v[part_of * V + i] : 0.f;
+    for (int base = m_first; base < m_last; base += kRows * side) {
+        float o[kRows], y0[kRows];
 #pragma unroll
-            for (int i = 0; i < V; i += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(v + k * V + i);
-                s = fmaf(br[i], f.x, s);
-                s = fmaf(br[i + 1], f.y, s);
-                s = fmaf(br[i + 2], f.z, s);
-                s = fmaf(br[i + 3], f.w, s);
-            }
+        for (int k = 0; k < kRows; ++k) {
+            o[k] = 0.f;
+            y0[k] = ys[k];
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[k] = fmaf(rows[k][i], mine[i], o[k]);
         }
-        out[m] = from_f32<T>(fmaf(scale, s, m == m0 ? y0 : to_f32(y[m])));
+        const int at = m;
+        m += kRows * side;
+        if (base + kRows * side < m_last) fetch(m);
+        for (int d = p.row_lanes / 2; d; d >>= 1)
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) o[k] += __shfl_xor_sync(~0u, o[k], d);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+            if (part_of == 0 && at + k * side < m_last)
+                out[at + k * side] = from_f32<T>(fmaf(scale, o[k], y0[k]));
     }
     cluster.barrier_wait(std::move(left));  // its own part may go once all have
 }
@@ -739,6 +746,8 @@ SPCONV_API int spconv_adapter_add(const spconv_adapter_args *a, void *stream) {
     if (a->P == 1) {
         p.vec_x = rows_aligned(a->x, a->x_stride_n, 0, e);
         p.vec_b = rows_aligned(a->b, 0, a->R, e);
+        p.row_lanes = 1;
+        while (p.row_lanes * 16 < (int)(a->R * e)) p.row_lanes *= 2;
         return by_dtype(a->dtype, [&](auto t) {
             return launch_clusters(token_kernel<decltype(t)>, p.N, ranks_for(p, p.N, 4 * kSMs, 64),
                                    kTokenThreads, 0, p, s);
