@@ -14,6 +14,8 @@
 // Prompts use matrix instructions on registers (mma.sync): with R <= 64 rows
 // an operand tile is far too small to keep the tensor memory path busy, and
 // the products take a fraction of the time of the reads and writes around them.
+// 8 x 1024 positions, 2048 -> 4096, rank 32 in bf16 take 39 us, 0.61 of the
+// measured bandwidth: a wave of clusters, whose two phases do not overlap.
 #include <cooperative_groups.h>
 
 #include <utility>

@@ -221,11 +221,103 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4) conv_kernel(
     }
 }
 
+// The gradients' loop of a thread whose items are the same whole, aligned run of
+// one full sequence after the other: what is special about the first and the
+// last run is known before it.
+template <typename T, int K, bool SILU>
+static __device__ __forceinline__ void back_whole_runs(const ConvParams &p, const float (&w)[K],
+                                                       float b, int c, int t0, int n0, int dn,
+                                                       float (&sum)[K + 1]) {
+    constexpr int kG = kVec + K - 1;
+    const bool is_first = t0 == 0, is_last = t0 + kVec == p.L;
+    int64_t row = (int64_t)n0 * p.C + c;
+    const int64_t row_step = (int64_t)dn * p.C, x_step = dn * p.x_sn, dy_step = dn * p.dy_sn;
+    const T *x = static_cast<const T *>(p.x) + n0 * p.x_sn + c * p.x_sc + t0;
+    const T *dy = static_cast<const T *>(p.dy) + n0 * p.dy_sn + c * p.dy_sc + t0;
+    T *dx = static_cast<T *>(p.dx) + row * p.L + t0;
+    const int64_t dx_step = row_step * p.L;
+    Run<T> left, right, gright;
+    left.clear();
+    right.clear();
+    gright.clear();
+    for (int64_t n = n0; n < p.N; n += dn, x += x_step, dy += dy_step, dx += dx_step, row += row_step) {
+        Run<T> in, gin;
+        load_run(in, x, 0, kVec, true);
+        load_run(gin, dy, 0, kVec, true);
+        if (K > 1 && !is_first) load_run(left, x - kVec, 0, kVec, true);
+        if (K > 1 && is_first && p.state) {
+            float f[kVec] = {};
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+                f[kVec - (K - 1) + j] = to_f32(static_cast<const T *>(p.state)[row * (K - 1) + j]);
+            left.put(f);
+        }
+        if (K > 1 && !is_last) {
+            load_run(right, x + kVec, 0, kVec, true);
+            load_run(gright, dy + kVec, 0, kVec, true);
+        }
+        float s[kG + K - 1], g[kG], o[kVec];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+            s[j] = left[kVec - (K - 1) + j];
+            s[K - 1 + kVec + j] = right[j];
+            g[kVec + j] = gright[j];
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            s[K - 1 + j] = in[j];
+            g[j] = gin[j];
+        }
+        if (SILU) {
+#pragma unroll
+            for (int j = 0; j < kG; ++j) {
+                float v = b;
+#pragma unroll
+                for (int k = 0; k < K; ++k) v = fmaf(w[k], s[j + k], v);
+                g[j] *= silu_grad(v);
+            }
+            if (K > 1 && is_last) {
+#pragma unroll
+                for (int j = kVec; j < kG; ++j) g[j] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            sum[K] += g[j];
+            o[j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                sum[k] = fmaf(g[j], s[j + k], sum[k]);
+                o[j] = fmaf(w[k], g[j + K - 1 - k], o[j]);
+            }
+        }
+        if (K > 1 && is_last && p.dfinal) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+                o[kVec - (K - 1) + j] += to_f32(static_cast<const T *>(p.dfinal)[row * (K - 1) + j]);
+        }
+        Run<T> out;
+        out.put(o);
+        *reinterpret_cast<Run<T> *>(dx) = out;
+        if (K > 1 && is_first && p.dstate) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {  // (a whole run: the sequence is longer than the state)
+                float d = 0.f;
+#pragma unroll
+                for (int k = 0; k <= j; ++k) d = fmaf(w[k], g[j - k], d);
+                static_cast<T *>(p.dstate)[row * (K - 1) + j] = from_f32<T>(d);
+            }
+        }
+    }
+}
+
 // Backward: a block takes every splits-th group of kThreads runs of one
 // channel over all sequences; a thread holds the inputs around its run, forms
 // g for its kVec positions and the K-1 behind them (which its right neighbour
 // forms too: K-1 in kVec twice is cheaper than an exchange), writes dx and
 // adds to its sums for dw and db.  The sums are joined in a fixed order.
+// Bound by its instructions: 4 x 2048 x 2048 in bf16 take 28 us, 38 without the
+// loop of its own for whole runs (60 instructions an element).
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParams p) {
     const int c = blockIdx.x / p.splits, split = blockIdx.x - c * p.splits;
@@ -244,6 +336,15 @@ __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParam
         const int first = split * kThreads + threadIdx.x;
         n = first / p.runs;
         run = first - (int)n * p.runs;
+    }
+    if (dr == 0 && p.vec_x && p.vec_dy && p.vec_y && !p.lengths && p.L % kVec == 0 && p.runs > 0) {
+        if (n < p.N) {
+            if (p.silu)
+                back_whole_runs<T, K, true>(p, w, b, c, run * kVec, (int)n, dn, sum);
+            else
+                back_whole_runs<T, K, false>(p, w, b, c, run * kVec, (int)n, dn, sum);
+        }
+        n = p.N;
     }
     int64_t rowi = n * p.C + c;
     const T *row = static_cast<const T *>(p.x) + n * p.x_sn + c * p.x_sc;

