@@ -23,7 +23,8 @@ namespace seq {
 
 constexpr int kSMs = 152;
 constexpr int kVec = 8;  // positions a thread holds of a row
-constexpr int kMaxLength = 0x7fffff00;  // positions of a sequence: tiles stay within 32 bits
+constexpr int kMaxLength = 0x7fff0000;  // positions of a sequence: a block's reach beyond stays
+                                        // within 32 bits
 
 // ---------------------------------------------------------------- elements
 

@@ -584,8 +584,11 @@ Layout plan(ScanParams &p) {
     // the time goes by waves x tiles; of equals the longest (it has the fewest shares
     // of dA and the fewest of g's states)
     int64_t best = 0;
+    p.tiles_per_segment = 8;
+    p.segments = (p.tiles + 7) / 8;
     for (int per = 1; per <= 8 && per <= p.tiles; ++per) {
         const int64_t segments = (p.tiles + per - 1) / per;
+        if (segments > 65535) continue;  // they go along grid z
         const int64_t waves = (blocks * p.N * segments + 2 * kSMs - 1) / (2 * kSMs);
         if (best && waves * per > best) continue;
         best = waves * per;
