@@ -14,8 +14,8 @@
 // Prompts use matrix instructions on registers (mma.sync): with R <= 64 rows
 // an operand tile is far too small to keep the tensor memory path busy, and
 // the products take a fraction of the time of the reads and writes around them.
-// 8 x 1024 positions, 2048 -> 4096, rank 32 in bf16 take 39 us, 0.61 of the
-// measured bandwidth: a wave of clusters, whose two phases do not overlap.
+// 8 x 1024 positions, 2048 -> 4096, rank 32 in bf16 take 39 us (0.61 of the
+// measured bandwidth; rank 64: 60 us): a wave of clusters, whose two phases do not overlap.
 #include <cooperative_groups.h>
 
 #include <utility>
@@ -80,13 +80,16 @@ static __device__ __forceinline__ void split_tf32(float v, uint32_t &hi, uint32_
     const float rest = v - __uint_as_float(hi);
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(fabsf(v) <= 3.402e38f ? rest : 0.f));
 }
-// two values as words of 16-bit parts: hi, and what hi leaves
-template <typename T>
-static __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = f32_to_word<T>(a, b);
-    const float2 h = word_to_f32<T>(hi);
-    lo = f32_to_word<T>(fabsf(h.x) <= 3.4e38f ? a - h.x : 0.f,
-                        fabsf(h.y) <= 3.4e38f ? b - h.y : 0.f);
+// two values as words of three bfloat16 parts, each what the ones before leave:
+// all 24 bits of both.  An infinity or NaN is all in the first.
+static __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&parts)[3]) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        parts[k] = f32_to_word<__nv_bfloat16>(a, b);
+        const float2 h = word_to_f32<__nv_bfloat16>(parts[k]);
+        a = fabsf(h.x) <= 3.4e38f ? a - h.x : 0.f;
+        b = fabsf(h.y) <= 3.4e38f ? b - h.y : 0.f;
+    }
 }
 
 static __device__ __forceinline__ uint32_t smem_address(const void *p) {
@@ -443,38 +446,30 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
     // out = y + scale b v.  Column q of the four tiles of eight that a warp
     // multiplies stands for position 8 (q / 2) + 2 tile + q % 2 of its half, so
     // that a lane's results are eight consecutive positions.
-    constexpr bool kHalf = std::is_same<T, __half>::value;
-    constexpr int KS = RT * 2;  // steps of eight rows of v
-    __shared__ float units[kHalf ? kPos : 1];
-    float unit[8];  // of the lane's positions
-    if constexpr (kHalf) {
-        // 16-bit floats do not reach as far as sums of their products: each position's
-        // v is scaled to at most 2 by a power of two, and its products back
-        if (threadIdx.x < kPos) {
-            float most = 0.f;
-            for (int r = 0; r < p.R; ++r) most = fmaxf(most, fabsf(v[r * G::kVPitch + threadIdx.x]));
-            const uint32_t e = __float_as_uint(most) & 0x7f800000u;
-            units[threadIdx.x] = e == 0 || e >= 0x7f000000u ? 1.f : __uint_as_float(e);
-        }
-        __syncthreads();
+    // v keeps its bits between the products.  Against bfloat16 it goes as three parts
+    // of that type.  Half precision does not reach as far as sums of its products,
+    // and one scale for a position's sums loses those 2^14 below the largest: so its
+    // b goes to the 32-bit instruction, which holds it, with v as two parts, and the rows
+    // of a step of eight in the order in which b's words hold them (8 x 1024 positions,
+    // 2048 -> 4096: rank 32 41 us, rank 64 82, its registers leave two blocks per SM;
+    // b as two bfloat16 parts against three of v took 46 and 85).
+    constexpr bool kHalf = std::is_same<T, __half>::value, kBf16 = kPairs && !kHalf;
+    constexpr int KS = kBf16 ? RT : RT * 2;  // steps of 16 or 8 rows of v
+    constexpr int kParts = kBf16 ? 3 : 2;
+    uint32_t vp[KS][4][2][kParts];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) unit[i] = units[(warp >> 1) * 32 + j * 8 + i];
-    }
-    uint32_t vh[KS][4][2], vl[KS][4][2];  // (16-bit: the words of steps 2k, 2k + 1 are one step of 16)
-#pragma unroll
-    for (int k = 0; k < (kPairs ? RT : KS); ++k)
+    for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            const int pos = (warp >> 1) * 32 + (g >> 1) * 8 + 2 * t + (g & 1);
-            const float *col = v + pos;
-            const float down = kHalf ? 1.f / units[kHalf ? pos : 0] : 1.f;
+            const float *col = v + (warp >> 1) * 32 + (g >> 1) * 8 + 2 * t + (g & 1);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if constexpr (kPairs) {
-                    const float *at2 = col + (k * 16 + i * 8 + 2 * j) * G::kVPitch;
-                    split_pair<T>(at2[0] * down, at2[G::kVPitch] * down, vh[k][t][i], vl[k][t][i]);
+                if constexpr (kBf16) {
+                    const float *two = col + (k * 16 + i * 8 + 2 * j) * G::kVPitch;
+                    split_bf16(two[0], two[G::kVPitch], vp[k][t][i]);
                 } else {
-                    split_tf32(col[(k * 8 + i * 4 + j) * G::kVPitch], vh[k][t][i], vl[k][t][i]);
+                    const int row = k * 8 + (kHalf ? 2 * j + i : i * 4 + j);
+                    split_tf32(col[row * G::kVPitch], vp[k][t][i][0], vp[k][t][i][1]);
                 }
             }
         }
@@ -506,13 +501,24 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
-        if constexpr (kPairs) {
+        if constexpr (kBf16) {
 #pragma unroll
-            for (int k = 0; k < RT; ++k) {
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int e = kParts - 1; e >= 0; --e)
+                        mma16<T>(acc[t], now[k], vp[k][t][0][e], vp[k][t][1][e]);
+        } else if constexpr (kHalf) {
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const uint32_t *w = now[k / 2] + k % 2 * 2;
+                const float2 w0 = word_to_f32<T>(w[0]), w1 = word_to_f32<T>(w[1]);
+                const uint32_t bh[4] = {bits_of(w0.x), bits_of(w1.x), bits_of(w0.y), bits_of(w1.y)};
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    mma16<T>(acc[t], now[k], vl[k][t][0], vl[k][t][1]);
-                    mma16<T>(acc[t], now[k], vh[k][t][0], vh[k][t][1]);
+                    mma8(acc[t], bh, vp[k][t][0][1], vp[k][t][1][1]);
+                    mma8(acc[t], bh, vp[k][t][0][0], vp[k][t][1][0]);
                 }
             }
         } else {
@@ -528,9 +534,9 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
                 }
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    mma8(acc[t], bl, vh[k][t][0], vh[k][t][1]);
-                    mma8(acc[t], bh, vl[k][t][0], vl[k][t][1]);
-                    mma8(acc[t], bh, vh[k][t][0], vh[k][t][1]);
+                    mma8(acc[t], bl, vp[k][t][0][0], vp[k][t][1][0]);
+                    mma8(acc[t], bh, vp[k][t][0][1], vp[k][t][1][1]);
+                    mma8(acc[t], bh, vp[k][t][0][0], vp[k][t][1][0]);
                 }
             }
         }
@@ -539,9 +545,8 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float up = kHalf ? scale * unit[2 * t + i] : scale;
-                f0[2 * t + i] = fmaf(up, acc[t][i], e0.get(2 * t + i));
-                f1[2 * t + i] = fmaf(up, acc[t][2 + i], e1.get(2 * t + i));
+                f0[2 * t + i] = fmaf(scale, acc[t][i], e0.get(2 * t + i));
+                f1[2 * t + i] = fmaf(scale, acc[t][2 + i], e1.get(2 * t + i));
             }
         if (r0 < p.M) e0.store(f0, o, 0, p.P - at, p.vec_y);
         if (r1 < p.M) e1.store(f1, o + y_half, 0, p.P - at, p.vec_y);
