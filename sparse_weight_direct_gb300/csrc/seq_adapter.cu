@@ -73,24 +73,31 @@ static __device__ __forceinline__ void mma8(float (&d)[4], const uint32_t (&a)[4
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// v = hi + lo, each of 11 bits: 22 of v's 24 bits.  An infinity or NaN is all
-// in hi.
+// v = hi + lo, each of 11 bits: 22 of v's 24 bits at least.
 static __device__ __forceinline__ void split_tf32(float v, uint32_t &hi, uint32_t &lo) {
     asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(v));
     const float rest = v - __uint_as_float(hi);
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(fabsf(v) <= 3.402e38f ? rest : 0.f));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(rest));
 }
 // two values as words of three bfloat16 parts, each what the ones before leave:
-// all 24 bits of both.  An infinity or NaN is all in the first.
+// all 24 bits of both
 static __device__ __forceinline__ void split_bf16(float a, float b, uint32_t (&parts)[3]) {
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         parts[k] = f32_to_word<__nv_bfloat16>(a, b);
         const float2 h = word_to_f32<__nv_bfloat16>(parts[k]);
-        a = fabsf(h.x) <= 3.4e38f ? a - h.x : 0.f;
-        b = fabsf(h.y) <= 3.4e38f ? b - h.y : 0.f;
+        a -= h.x;
+        b -= h.y;
     }
 }
+// Sums of parts' products are NaN where the whole ones' are an infinity (a part of
+// zero, or of the other sign, against it) or near the largest value (whose first
+// part rounds beyond it).  So sums that are not finite are formed again from whole
+// products.
+static __device__ __forceinline__ bool finite4(float a, float b, float c, float d) {
+    return fmaf(a, 0.f, b * 0.f) + fmaf(c, 0.f, d * 0.f) == 0.f;
+}
+static __device__ __forceinline__ bool finite(float v) { return fabsf(v) <= 3.40282347e38f; }
 
 static __device__ __forceinline__ uint32_t smem_address(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -139,6 +146,9 @@ struct PromptTile {
     static constexpr int kFront =
         kStages * kStage > kV + kRing ? kStages * kStage : kV + kRing;
     static constexpr int kSmem = kFront + kV;
+    // Blocks of an SM that registers are held to where the compiler would take more
+    // (0: as it likes).
+    static constexpr int kBlocks = kWide ? 0 : std::is_same<T, __half>::value ? (RT == 2) * 4 : (RT == 4) * 3;
 };
 
 // One stage: kChan channels from c0 of the tile's positions and of a's rows.
@@ -206,7 +216,7 @@ struct Eight {
 };
 
 template <typename T, int RT>
-__global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p) {
+__global__ void __launch_bounds__(kThreads, PromptTile<T, RT>::kBlocks) prompt_kernel(const AdapterParams p) {
     using G = PromptTile<T, RT>;
     constexpr bool kWide = G::kWide;
     constexpr int kChan = G::kChan;
@@ -419,11 +429,30 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
                         row < p.R ? acc[r][q][i] : 0.f;
                 }
     }
+    // four positions of a row of v; 16-bit factors are whole in the instruction
+    auto place_of = [](int i) { return i / (kPos / 4) * G::kVPitch + i % (kPos / 4) * 4; };
+    auto form_again = [&](int i, float4 &t) {
+        if (!kWide || finite4(t.x, t.y, t.z, t.w)) return;
+        const int row = i / (kPos / 4), first = p0 + i % (kPos / 4) * 4;
+        if (row >= p.R) return;
+        float sum[4] = {};
+#pragma unroll 4
+        for (int c = 0; c < p.C; ++c) {
+            const float f = to_f32(a[(int64_t)row * p.C + c]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (first + q < p.P) sum[q] = fmaf(f, to_f32(x[c * p.x_sc + first + q]), sum[q]);
+        }
+        t.x = finite(t.x) ? t.x : sum[0];
+        t.y = finite(t.y) ? t.y : sum[1];
+        t.z = finite(t.z) ? t.z : sum[2];
+        t.w = finite(t.w) ? t.w : sum[3];
+    };
     if (ranks > 1) {
         cluster.sync();
         // each block adds a share of v over the ranks and hands it to all
         for (int i = rank * kThreads + threadIdx.x; i < G::RP * kPos / 4; i += ranks * kThreads) {
-            const int o = i / (kPos / 4) * G::kVPitch + i % (kPos / 4) * 4;
+            const int o = place_of(i);
             float4 f[kMaxRanks], t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kMaxRanks; ++k)  // read together, added in their order
@@ -433,6 +462,7 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
             for (int k = 0; k < kMaxRanks; ++k) {
                 t.x += f[k].x; t.y += f[k].y; t.z += f[k].z; t.w += f[k].w;
             }
+            form_again(i, t);
 #pragma unroll
             for (int k = 0; k < kMaxRanks; ++k)
                 if (k < ranks) *reinterpret_cast<float4 *>(cluster.map_shared_rank(v, k) + o) = t;
@@ -441,6 +471,11 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
     } else {
         v = part;
         __syncthreads();
+        if (kWide) {
+            for (int i = threadIdx.x; i < G::RP * kPos / 4; i += kThreads)
+                form_again(i, *reinterpret_cast<float4 *>(part + place_of(i)));
+            __syncthreads();
+        }
     }
 
     // out = y + scale b v.  Column q of the four tiles of eight that a warp
@@ -451,7 +486,7 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
     // and one scale for a position's sums loses those 2^14 below the largest: so its
     // b goes to the 32-bit instruction, which holds it, with v as two parts, and the rows
     // of a step of eight in the order in which b's words hold them (8 x 1024 positions,
-    // 2048 -> 4096: rank 32 41 us, rank 64 82, its registers leave two blocks per SM;
+    // 2048 -> 4096: rank 32 42 us, rank 64 82, its registers leave two blocks per SM;
     // b as two bfloat16 parts against three of v took 46 and 85).
     constexpr bool kHalf = std::is_same<T, __half>::value, kBf16 = kPairs && !kHalf;
     constexpr int KS = kBf16 ? RT : RT * 2;  // steps of 16 or 8 rows of v
@@ -475,17 +510,27 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         }
     int slot = 0;
     T *o = out + (int64_t)(m_own * 16 + g) * p.P + at;
-    for (int m = m_own; m < m_last; m += 2, o += y_step) {
+    int m = m_own;
+    for (; m < m_last; m += 2, o += y_step) {
         const int r0 = m * 16 + g, r1 = r0 + 8;
         Eight<T> e0, e1;
-        if (p.vec_y) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-            e0.read(ring + slot * 512);
-            e1.read(ring + slot * 512 + 256);
-        } else {
-            e0.load(y + (int64_t)r0 * p.P, at, r0 < p.M ? p.P : 0, false);
-            e1.load(y + (int64_t)r1 * p.P, at, r1 < p.M ? p.P : 0, false);
-        }
+        auto read_y = [&]() {
+            if (p.vec_y) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+                e0.read(ring + slot * 512);
+                e1.read(ring + slot * 512 + 256);
+            } else {
+                e0.load(y + (int64_t)r0 * p.P, at, r0 < p.M ? p.P : 0, false);
+                e1.load(y + (int64_t)r1 * p.P, at, r1 < p.M ? p.P : 0, false);
+            }
+        };
+        auto more_y = [&]() {
+            fetch_y(slot);
+            slot = slot + 1 < kDepth ? slot + 1 : 0;
+        };
+        // (behind the products of 16-bit types, where its registers are short: bf16
+        // rank 64 68 -> 60 us; before those of 32 bits, which wait for it: rank 64 221 -> 205)
+        if (kWide) read_y();
         uint32_t now[kPairs ? RT : kAhead ? 2 * RT : 1][4];
         if constexpr (kAhead) {
 #pragma unroll
@@ -494,8 +539,7 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
                 for (int i = 0; i < 4; ++i) now[k][i] = next[k][i];
         }
         fetch_b(m + 2);
-        fetch_y(slot);
-        slot = slot + 1 < kDepth ? slot + 1 : 0;
+        if (kWide) more_y();
         float acc[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -540,6 +584,12 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
                 }
             }
         }
+        if (!kWide) read_y();
+        bool fine = true;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) fine &= finite4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+        if (__any_sync(~0u, !fine)) break;
+        if (!kWide) more_y();
         float f0[8], f1[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
@@ -551,6 +601,26 @@ __global__ void __launch_bounds__(kThreads) prompt_kernel(const AdapterParams p)
         if (r0 < p.M) e0.store(f0, o, 0, p.P - at, p.vec_y);
         if (r1 < p.M) e1.store(f1, o + y_half, 0, p.P - at, p.vec_y);
     }
+    if (m >= m_last) return;
+    // the warp's rows from one on whose sums are not finite, by whole products
+    // (behind the loop: in it they cost registers, and with them blocks of an SM)
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    const float *col = v + (warp >> 1) * 32 + j * 8;
+    for (; m < m_last; m += 2)
+        for (int row = m * 16 + g; row < min(m * 16 + 16, p.M); row += 8) {
+            const T *q = b + (int64_t)row * p.R;
+            float f[8] = {};
+            for (int r = 0; r < p.R; ++r) {
+                const float w = to_f32(q[r]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = fmaf(w, col[r * G::kVPitch + i], f[i]);
+            }
+            Eight<T> e;
+            e.load(y + (int64_t)row * p.P, at, p.P, p.vec_y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = fmaf(scale, f[i], e.get(i));
+            e.store(f, out + (int64_t)row * p.P, at, p.P, p.vec_y);
+        }
 }
 
 // ---------------------------------------------------------------- single tokens

@@ -72,3 +72,78 @@ def test_adapter_differences_of_large_whole_sums(dtype, R, P):
     assert float(v.abs().max()) >= 1 << 16 and float(want.abs().max()) <= 256
     out = swd.adapter_add(y, x, a, b, index.cuda())
     assert torch.equal(out.cpu().double(), want)
+
+
+# ------------------------------------------------------------------ adapters: infinities
+
+
+def same_values(got, want, bound, open_, what):
+    """NaN where `want` is, infinities alike, the rest within the bound; nothing
+    is asked where it is open."""
+    got, want, bound = (torch.where(open_.to(t.device), torch.zeros_like(t), t) for t in (got, want, bound))
+    g, fine = ref.f64(got), torch.isfinite(want)
+    assert torch.equal(torch.isnan(g), torch.isnan(want)), what
+    assert torch.equal(g[torch.isinf(want)], want[torch.isinf(want)]), what
+    zero = torch.zeros_like(want)
+    ref.check(torch.where(fine.to(got.device), got, torch.zeros_like(got)), torch.where(fine, want, zero),
+              torch.where(fine, bound, zero), what)
+
+
+INF = float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [1, 2, 40, 64])
+@pytest.mark.parametrize("R", [1, 8, 33])
+@pytest.mark.parametrize("dtype", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("where", ["x", "a", "b", "x and a", "x largest", "v overflows", "scale"])
+def test_adapter_infinities(dtype, R, P, where):
+    """One infinite input reaches the outputs that its products reach with the
+    sign that the definition gives it, whatever the other factor's bits, and no
+    other position, row or request.  Rows of one term: no other term hides it."""
+    d = Draw(33)
+    N, C, M, K = 3, 20, 24, 2
+    most = torch.finfo(dtype).max
+    x, y, scale = d(N, C, P, dtype=dtype), d(N, M, P, dtype=dtype), torch.ones(K, device="cuda")
+    a, b = d(K, R, C, dtype=dtype), d(K, M, R, dtype=dtype)
+    # factors that meet the infinity: whole in few bits, and not
+    some = torch.tensor([0.5, 0.3, -0.3, 0.001, -2.0, 1.0, 3.0, -0.7], device="cuda")
+    a[:, :, 3], b[:, :, 0] = some[torch.arange(R) % 8].to(dtype), some[torch.arange(M) % 8].to(dtype)
+    x[:, 3, :] = some[(torch.arange(P) + 2) % 8].to(dtype)
+    if "x" in where.split():
+        x[0, 3, P // 2] = most if "largest" in where else -INF
+    if "a" in where.split():
+        a[0, 0, 3] = INF
+    if where == "b":
+        b[0, 5, 0] = -INF
+        b[0, 7, R - 1] = INF
+    if where == "v overflows":  # (of 32-bit sums: not from half precision)
+        x[0, 3, P // 2], a[0, 0, 3] = most, most
+    if where == "scale":
+        scale[0] = INF
+    index = torch.tensor([0, 1, -1], dtype=torch.int32)
+    out = swd.adapter_add(y, x, a, b, index.cuda(), scale=scale)
+    # the definition in 32 bits (an overflow is one), then in 64 for the finite values
+    # (by plain sums: a library's product may split its terms)
+    v = (a.float()[[0, 1, 0], :, :, None] * x.float()[:, None]).sum(2)
+    far, size = torch.zeros(N, M, P, device="cuda"), torch.zeros(N, M, P, device="cuda")
+    for r in range(R):
+        br, vr = b.float()[[0, 1, 0], :, r, None], v[:, None, r]
+        far, size = far + br * vr, size + torch.where(torch.isfinite(br) & torch.isfinite(vr), (br * vr).abs(), 0.0)
+    far = y.float() + scale[[0, 1, 0], None, None] * far
+    want, bound = ref.adapter(y, x, a, b, index, scale)
+    far = ref.f64(far)
+    far[2] = ref.f64(y)[2]
+    want = torch.where(torch.isfinite(far), want, far)
+    # a finite result half a unit beyond the type's largest rounds to an infinity
+    edge = most * (1 + torch.finfo(dtype).eps / 4 / (1 - torch.finfo(dtype).eps / 2))
+    bound = torch.where(torch.isfinite(bound), bound, torch.zeros_like(bound))
+    # open: what finite terms add up to where their sum may overflow in one order
+    # and not in another, and the side of that edge that a sum ends on
+    open_ = (want.abs() - edge).abs() <= bound
+    if R > 1:
+        open_ |= torch.isinf(ref.f64(size))
+    open_[2] = False
+    want = torch.where(want.abs() >= edge, torch.sign(want) * INF, want)
+    same_values(out, want, bound, open_, where)
+    assert R > 1 or where not in ("x", "b") or torch.isinf(want).any()
