@@ -9,8 +9,11 @@ bfloat16 or float16, all of one call alike; weights, their gradients and the
 scan's states are float32.
 
 Like ``forward``, these calls only marshal pointers: every step runs in
-libspconv.so, asynchronously on ``stream`` (default: the current torch
-stream), and a wrong argument raises SpconvError before any work is enqueued.
+libspconv.so, asynchronously on ``stream`` (a torch stream or its handle;
+default: the current torch stream), and a wrong argument raises SpconvError
+before any work is enqueued.  Like every torch operation, a call on another
+stream waits for nothing: its inputs have to be ready there, and whoever reads
+its outputs elsewhere waits for that stream.
 """
 from __future__ import annotations
 
@@ -97,28 +100,45 @@ def _dims(t, count, name):
     return t.shape
 
 
-def _run(function, args, device, stream, tensors, query=None):
-    """Enqueues a call on its stream.  On a stream other than the current one the
-    call's tensors are marked as used there, so that their memory is not given
-    out again before the stream has passed the call."""
-    current = _raw_stream(device)
-    ptr = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
-    workspace = None
+def _run(function, args, device, query=None):
+    """Enqueues a call on the current stream."""
     if query is not None:
         need = query(args + _no_workspace)
         if need:
             workspace = _empty(need, dtype=_torch.uint8, device=device)
         args += _pack_workspace(workspace.data_ptr(), need) if need else _no_workspace
-    rc = function(args, ptr)
+    rc = function(args, _raw_stream(device))
     if rc:
         _lib.check(rc, function.__name__)
-    if ptr != current:
-        on = stream
-        if isinstance(stream, int):
-            on = _torch.cuda.ExternalStream(ptr) if ptr else _torch.cuda.default_stream(device)
-        for t in (*tensors, workspace):
-            if t is not None:
-                t.record_stream(on)
+
+
+def _elsewhere(call, stream, given, named):
+    """The call with `stream` as the current one, so that its outputs and its
+    workspace come from memory that this stream's own work is done with: a block
+    that was given back to the caller's stream may still be read there.  Its
+    tensors are marked as used on the other of the two streams, so that their
+    memory is not given out again before that has passed what it holds now."""
+    if _torch is None:
+        _load()
+    if not isinstance(given[0], _Tensor) or not given[0].is_cuda:
+        return call(*given, **named)  # (refused)
+    cuda = _torch.cuda
+    current, on = cuda.current_stream(), stream
+    if not isinstance(stream, cuda.Stream):
+        ptr = stream if isinstance(stream, int) else stream.cuda_stream
+        on = cuda.ExternalStream(ptr) if ptr else cuda.default_stream()
+    if on.cuda_stream == current.cuda_stream:
+        return call(*given, **named)
+    with cuda.stream(on):
+        result = call(*given, **named)
+    for t in (*given, *named.values()):
+        if isinstance(t, _Tensor):
+            t.record_stream(on)
+    outputs = result.values() if isinstance(result, dict) else result if isinstance(result, tuple) else (result,)
+    for t in outputs:
+        if t is not None:
+            t.record_stream(current)
+    return result
 
 
 def short_conv(x, weight, bias=None, *, silu: bool = True, state=None, final_state=None,
@@ -129,6 +149,9 @@ def short_conv(x, weight, bias=None, *, silu: bool = True, state=None, final_sta
     float32; state: (N, C, K-1), the inputs before x; lengths: (N,) int32, outputs behind
     them are zero; final_state (optional, same shape as state): overwritten
     with the state behind the last position.  Returns y (``out`` if given)."""
+    if stream is not None:
+        return _elsewhere(short_conv, stream, (x, weight, bias),
+                          dict(silu=silu, state=state, final_state=final_state, lengths=lengths, out=out))
     dt, code, dev = _begin(x, "x", 3)
     shape = N, C, L = x.shape
     K = _dims(weight, 2, "weight")[1]
@@ -141,8 +164,7 @@ def short_conv(x, weight, bias=None, *, silu: bool = True, state=None, final_sta
         _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
         _whole(lengths, "lengths", _i32, dev, (N,)), 0, _whole(out, "out", dt, dev, shape),
         _whole(final_state, "final_state", dt, dev, st), 0, 0, 0, 0, 0, 0, 0)
-    _run(_library.spconv_short_conv, args + _no_workspace, dev, stream,
-         (x, weight, bias, state, lengths, out, final_state))
+    _run(_library.spconv_short_conv, args + _no_workspace, dev)
     return out
 
 
@@ -151,6 +173,9 @@ def short_conv_backward(dy, x, weight, bias=None, *, silu: bool = True, state=No
     """Gradients of ``short_conv`` called with the same arguments, from those of
     y (dy) and, optionally, of final_state: (dx, dweight, dbias, dstate), with
     None for dbias without a bias and for dstate without a state."""
+    if stream is not None:
+        return _elsewhere(short_conv_backward, stream, (dy, x, weight, bias),
+                          dict(silu=silu, state=state, dfinal_state=dfinal_state, lengths=lengths))
     dt, code, dev = _begin(x, "x", 3)
     shape = N, C, L = x.shape
     K = _dims(weight, 2, "weight")[1]
@@ -166,8 +191,7 @@ def short_conv_backward(dy, x, weight, bias=None, *, silu: bool = True, state=No
         _whole(lengths, "lengths", _i32, dev, (N,)), 0, 0, 0, 0, dy_at,
         _whole(dfinal_state, "dfinal_state", dt, dev, st), dx.data_ptr(),
         0 if ds is None else ds.data_ptr(), dw.data_ptr(), 0 if db is None else db.data_ptr())
-    _run(_library.spconv_short_conv_backward, args, dev, stream,
-         (dy, x, weight, bias, state, lengths, dfinal_state, dx, dw, db, ds),
+    _run(_library.spconv_short_conv_backward, args, dev,
          _library.spconv_short_conv_backward_workspace)
     return dx, dw, db, ds
 
@@ -178,6 +202,9 @@ def short_conv_step(x, state, weight, bias=None, *, silu: bool = True, slots=Non
     (num_slots, C, K-1) moved on in place.  Request n uses state slots[n] ((N,)
     int32; None: number n); one whose slot is outside gets zeros and changes
     nothing."""
+    if stream is not None:
+        return _elsewhere(short_conv_step, stream, (x, state, weight, bias),
+                          dict(silu=silu, slots=slots, out=out))
     dt, code, dev = _begin(x, "x", 2)
     shape = N, C = x.shape
     K = _dims(weight, 2, "weight")[1]
@@ -189,8 +216,7 @@ def short_conv_step(x, state, weight, bias=None, *, silu: bool = True, slots=Non
         N, C, 1, K, code, silu, pool, 0, xn, 1, 0, 0, x_at, _whole(weight, "weight", _f32, dev, (C, K)), _whole(bias, "bias", _f32, dev, (C,)), 0, 0,
         _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape), 0,
         _whole(state, "state", dt, dev, (pool, C, K - 1)), 0, 0, 0, 0, 0, 0)
-    _run(_library.spconv_short_conv_step, args + _no_workspace, dev, stream,
-         (x, weight, bias, slots, out, state))
+    _run(_library.spconv_short_conv_step, args + _no_workspace, dev)
     return out
 
 
@@ -241,6 +267,9 @@ def scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool =
 
     lengths: (N,) int32, outputs behind them are zero; final_state (optional):
     overwritten with h behind the last position.  Returns y."""
+    if stream is not None:
+        return _elsewhere(scan, stream, (u, delta, A, B, C, D, z, delta_bias),
+                          dict(softplus=softplus, state=state, final_state=final_state, lengths=lengths, out=out))
     dt, code, dev = _begin(u, "u", 3)
     shape = u.shape
     given, S, _ = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, False, 0)
@@ -251,8 +280,7 @@ def scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool =
         *given, _whole(state, "state", _f32, dev, states),
         _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, _whole(out, "out", dt, dev, shape),
         _whole(final_state, "final_state", _f32, dev, states), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    _run(_library.spconv_scan, args, dev, stream,
-         (u, delta, A, B, C, D, z, delta_bias, state, lengths, out, final_state),
+    _run(_library.spconv_scan, args, dev,
          _library.spconv_scan_workspace)
     return out
 
@@ -262,6 +290,9 @@ def scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, sof
     """Gradients of ``scan`` called with the same arguments, from those of y (dy)
     and, optionally, of final_state: a dict of du, ddelta, dA, dB, dC, dD, dz,
     ddelta_bias and dstate, None for an argument that was not given."""
+    if stream is not None:
+        return _elsewhere(scan_backward, stream, (dy, u, delta, A, B, C, D, z, delta_bias),
+                          dict(softplus=softplus, state=state, dfinal_state=dfinal_state, lengths=lengths))
     dt, code, dev = _begin(u, "u", 3)
     shape = u.shape
     if dy is None:
@@ -281,8 +312,7 @@ def scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, sof
         _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, 0, 0, 0, dy_at,
         _whole(dfinal_state, "dfinal_state", _f32, dev, states), at["du"], at["ddelta"], at["dz"],
         at["dB"], at["dC"], at["dA"], at["dD"], at["ddelta_bias"], at["dstate"])
-    _run(_library.spconv_scan_backward, args, dev, stream,
-         (dy, u, delta, A, B, C, D, z, delta_bias, state, lengths, dfinal_state, *g.values()),
+    _run(_library.spconv_scan_backward, args, dev,
          _library.spconv_scan_backward_workspace)
     return g
 
@@ -293,6 +323,9 @@ def scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, soft
     (N, S) or (N, groups, S) -> y (N, channels); ``state`` (num_slots,
     channels, S) float32 is moved on in place.  slots as for
     ``short_conv_step``."""
+    if stream is not None:
+        return _elsewhere(scan_step, stream, (state, u, delta, A, B, C, D, z, delta_bias),
+                          dict(softplus=softplus, slots=slots, out=out))
     dt, code, dev = _begin(u, "u", 2)
     shape = N, ch = u.shape
     pool = _dims(state, 3, "state")[0]
@@ -302,8 +335,7 @@ def scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, soft
     args = _pack_scan(
         *given, 0, 0, _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape),
         0, _whole(state, "state", _f32, dev, (pool, ch, S)), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    _run(_library.spconv_scan_step, args + _no_workspace, dev, stream,
-         (u, delta, A, B, C, D, z, delta_bias, slots, out, state))
+    _run(_library.spconv_scan_step, args + _no_workspace, dev)
     return out
 
 
@@ -314,6 +346,8 @@ def adapter_add(y, x, a, b, index, *, scale=None, out=None, stream=None):
     projection's output, (N, M, P) or (N, M); a: (adapters, R, C) and b:
     (adapters, M, R) of x's type, R = 1..64; index: (N,) int32; scale:
     (adapters,) float32, 1 if None.  out may be y itself.  Returns out."""
+    if stream is not None:
+        return _elsewhere(adapter_add, stream, (y, x, a, b, index), dict(scale=scale, out=out))
     single = getattr(x, "ndim", 0) == 2
     dt, code, dev = _begin(x, "x", 2 if single else 3)
     N, C = x.shape[0], x.shape[1]
@@ -331,5 +365,5 @@ def adapter_add(y, x, a, b, index, *, scale=None, out=None, stream=None):
         N, P, C, M, R, K, code, 0, xs[0], xs[1], x_at, _whole(a, "a", dt, dev, (K, R, C)), _whole(b, "b", dt, dev, (K, M, R)),
         _whole(index, "index", _i32, dev, (N,)), _whole(scale, "scale", _f32, dev, (K,)), y_at,
         _whole(out, "out", dt, dev, shape))
-    _run(_library.spconv_adapter_add, args, dev, stream, (y, x, a, b, index, scale, out))
+    _run(_library.spconv_adapter_add, args, dev)
     return out

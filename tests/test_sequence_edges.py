@@ -147,3 +147,117 @@ def test_adapter_infinities(dtype, R, P, where):
     want = torch.where(want.abs() >= edge, torch.sign(want) * INF, want)
     same_values(out, want, bound, open_, where)
     assert R > 1 or where not in ("x", "b") or torch.isinf(want).any()
+
+
+# ------------------------------------------------------------------ another stream
+
+
+def calls_on_streams():
+    """name -> call(stream), its inputs made ready."""
+    d = Draw(41)
+    N, C, L, S = 2, 48, 512, 16
+    x, dy, w, b = d(N, C, L), d(N, C, L), d(C, 4), d(C)
+    A, B, Cm = -d(C, S).abs(), d(N, S, L), d(N, S, L)
+    y, a, bb, index = d(N, 40, L), d(2, 8, C), d(2, 40, 8), torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+    one = x[..., 0].contiguous()
+    pool, states = d(N, C, 3), d(N, C, S)
+    step = (one, one * 0.1, A, B[..., 0].contiguous(), Cm[..., 0].contiguous())
+    return {
+        "short_conv": lambda s: swd.short_conv(x, w, b, stream=s),
+        "short_conv_backward": lambda s: swd.short_conv_backward(dy, x, w, b, stream=s),
+        "short_conv_step": lambda s: swd.short_conv_step(one, pool.clone() if s is None else pool, w, b, stream=s),
+        "scan": lambda s: swd.scan(x, x * 0.1 if s is None else x, A, B, Cm, stream=s),
+        "scan_backward": lambda s: swd.scan_backward(dy, x, x, A, B, Cm, stream=s),
+        "scan_step": lambda s: swd.scan_step(states.clone() if s is None else states, *step, stream=s),
+        "adapter_add": lambda s: swd.adapter_add(y, x, a, bb, index, stream=s),
+    }
+
+
+def tensors_of(result):
+    if isinstance(result, dict):
+        result = tuple(result.values())
+    return [t for t in (result if isinstance(result, tuple) else (result,)) if t is not None]
+
+
+def busy(steps=20):
+    """Some tens of milliseconds of work on the current stream."""
+    m = torch.full((4096, 4096), 1.0 / 4096, device="cuda")
+    out = torch.empty_like(m)
+
+    def go():
+        for _ in range(steps):
+            torch.mm(m, m, out=out)
+    go()
+    torch.cuda.synchronize()
+    return go
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+@pytest.mark.parametrize("name", ["short_conv", "short_conv_backward", "short_conv_step", "scan", "scan_backward",
+                                  "scan_step", "adapter_add"])
+def test_memory_that_the_current_stream_still_reads(name, raw, monkeypatch):
+    """Tensors of the sizes that a call allocates are copied out at the end of a
+    long queue on the current stream and given back; a call on an independent
+    stream, which waits for nothing, leaves them alone."""
+    from sparse_weight_direct_gb300 import sequence
+    call = calls_on_streams()[name]
+    call(None)  # (torch is loaded by the first call)
+    sizes = []
+    with monkeypatch.context() as m:
+        for f in ("_empty", "_empty_like"):
+            plain = getattr(sequence, f)
+
+            def spy(*args, _plain=plain, **more):
+                t = _plain(*args, **more)
+                sizes.append(t.numel() * t.element_size())
+                return t
+            m.setattr(sequence, f, spy)
+        first = call(None)
+    assert sizes
+    work = busy()
+    side = torch.cuda.Stream()
+    del first
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    victims = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+    kept = [torch.zeros_like(v) for v in victims]
+    torch.cuda.synchronize()
+    work()
+    for k, v in zip(kept, victims):
+        k.copy_(v)
+    end = torch.cuda.Event()
+    end.record()
+    del victims, v
+    got = tensors_of(call(side.cuda_stream if raw else side))
+    early = not end.query()
+    torch.cuda.synchronize()
+    assert early, "the queue was too short to show anything"
+    for k in kept:
+        assert bool((k == 7).all())
+    assert got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["short_conv", "short_conv_backward", "scan", "scan_backward", "adapter_add"])
+def test_outputs_of_another_stream_given_back_while_read(name):
+    """Outputs that the current stream still reads when they are given back are not
+    overwritten by the next call on the stream that made them."""
+    call = calls_on_streams()[name]
+    work, side = busy(), torch.cuda.Stream()
+    first = tensors_of(call(side))
+    torch.cuda.synchronize()
+    want = [t.clone() for t in first]
+    kept = [torch.empty_like(t) for t in first]
+    torch.cuda.synchronize()
+    work()
+    for k, t in zip(kept, first):
+        k.copy_(t)
+    del first, t
+    with torch.cuda.stream(side):
+        junk = [torch.full_like(k, float("nan")) for k in kept]
+    again = tensors_of(call(side))
+    torch.cuda.synchronize()
+    del junk, again
+    for k, w in zip(kept, want):
+        assert torch.equal(k, w)
