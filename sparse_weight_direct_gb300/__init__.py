@@ -169,6 +169,25 @@ def _stream_ptr(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty_on(stream, shape, device):
+    """A float32 tensor for a call on `stream`.  On another stream than the
+    current one it comes from memory that this stream's own work is done with (a
+    block given back to the current stream may still be read there), and is kept
+    for what the current stream has queued when it is given back."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, device=device, dtype=torch.float32)
+    current = torch.cuda.current_stream(device)
+    ptr = _stream_ptr(stream).value or 0
+    if ptr == current.cuda_stream:
+        return torch.empty(shape, device=device, dtype=torch.float32)
+    with torch.cuda.stream(torch.cuda.ExternalStream(ptr, device=device) if ptr
+                           else torch.cuda.default_stream(device)):
+        out = torch.empty(shape, device=device, dtype=torch.float32)
+    out.record_stream(current)
+    return out
+
+
 def forward(x, packed: PackedWeights, out=None, stream=None, bias=None, relu: bool = False):
     """Y = conv(x, packed) on the GPU.  x: (N, C, H, W) contiguous float32
     CUDA tensor; out (optional): (N, M, E, F) float32 CUDA tensor, overwritten.
@@ -185,7 +204,7 @@ def forward(x, packed: PackedWeights, out=None, stream=None, bias=None, relu: bo
     E = out_extent(sh["H"], sh["R"], sh["stride"], sh["pad"])
     F = out_extent(sh["W"], sh["S"], sh["stride"], sh["pad"])
     if out is None:
-        out = torch.empty((N, sh["M"], E, F), device=x.device, dtype=torch.float32)
+        out = _empty_on(stream, (N, sh["M"], E, F), x.device)
     elif not (out.is_cuda and out.dtype == torch.float32 and out.is_contiguous()
               and tuple(out.shape) == (N, sh["M"], E, F)):
         raise SpconvError(_lib.SPCONV_ERR_INVALID_ARG, "out has the wrong shape/dtype/layout")

@@ -261,3 +261,33 @@ def test_outputs_of_another_stream_given_back_while_read(name):
     del junk, again
     for k, w in zip(kept, want):
         assert torch.equal(k, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_forward_leaves_memory_that_the_current_stream_still_reads(raw):
+    """The convolution's output, where the call allocates it."""
+    import workloads
+    L = workloads.LAYERS["tiny"]
+    w = swd.pack(*workloads.make_weights(L), C=L.C, H=L.H, W=L.W, M=L.M, R=L.R, S=L.S, stride=L.stride, pad=L.pad)
+    x = torch.from_numpy(workloads.make_input(L)).cuda()
+    want = swd.forward(x, w)
+    work, side = busy(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    victims = [torch.full_like(want, 7) for _ in range(2)]
+    kept = [torch.zeros_like(want) for _ in victims]
+    torch.cuda.synchronize()
+    work()
+    for k, v in zip(kept, victims):
+        k.copy_(v)
+    end = torch.cuda.Event()
+    end.record()
+    del victims, v
+    got = swd.forward(x, w, stream=side.cuda_stream if raw else side)
+    early = not end.query()
+    torch.cuda.synchronize()
+    assert early, "the queue was too short to show anything"
+    for k in kept:
+        assert bool((k == 7).all())
+    assert torch.equal(got, want)
+    w.close()
