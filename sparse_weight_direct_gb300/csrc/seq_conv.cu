@@ -583,7 +583,7 @@ SPCONV_API int spconv_short_conv(const spconv_short_conv_args *a, void *stream) 
     const int64_t rows = (int64_t)a->N * a->C;
     if (rows == 0) return SPCONV_OK;
     const size_t e = dtype_size(a->dtype);
-    if (a->L > 0 && (!a->x || !a->weight || !a->y)) return SPCONV_ERR_INVALID_ARG;
+    if (!a->weight || (a->L > 0 && (!a->x || !a->y))) return SPCONV_ERR_INVALID_ARG;
     if (!on_elements(a, {a->x, a->state, a->y, a->final_state}) ||
         !on_words({a->weight, a->bias, a->lengths}))
         return SPCONV_ERR_INVALID_ARG;

@@ -1,13 +1,16 @@
 """The sequence operators where values, sizes or streams are out of the ordinary:
 sums of very different size, infinities, memory of another stream, sizes near
 2^31, outputs that overlap what a call reads."""
+import ctypes
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import sequence_reference as ref  # noqa: E402
 import sparse_weight_direct_gb300 as swd  # noqa: E402
-from test_sequence import BF16, F16, F32, TYPE_IDS, TYPES, Draw  # noqa: E402
+from sparse_weight_direct_gb300 import _lib  # noqa: E402
+from test_sequence import F32, TYPE_IDS, TYPES, Draw, adapter_args, conv_args, scan_args  # noqa: E402
 
 # ------------------------------------------------------------------ adapters: sums of very different size
 
@@ -291,3 +294,17 @@ def test_forward_leaves_memory_that_the_current_stream_still_reads(raw):
         assert bool((k == 7).all())
     assert torch.equal(got, want)
     w.close()
+
+
+# ------------------------------------------------------------------ refusals at the C entry
+
+
+def refused(name, args):
+    return getattr(_lib.lib(), name)(ctypes.byref(args), None)
+
+
+def test_conv_without_positions_needs_its_weight():
+    """The kernel that writes the final state reads the weight: a call without one
+    is refused, with or without positions."""
+    assert refused("spconv_short_conv", conv_args(L=0, weight=None)) == _lib.SPCONV_ERR_INVALID_ARG
+    assert refused("spconv_short_conv", conv_args(L=0, weight=None, final_state=None)) == _lib.SPCONV_ERR_INVALID_ARG
