@@ -438,7 +438,8 @@ int spconv_packed_copy_array(const spconv_packed *p, int which, void *dst, int64
  *    is 16-byte aligned device memory that the caller keeps until the stream
  *    has passed the call.
  *  - Limits: K <= 4 taps, S <= 64 states, rank R <= 64, N <= 65535 for the scan
- *    and the steps, C, M and P <= 2^26 for the adapters.
+ *    and the steps, C, M and P <= 2^26 for the adapters, sequences, channels and
+ *    positions <= 2^31 - 2^16.
  *  - Errors: INVALID_ARG (a NULL or misaligned pointer, a negative size or
  *    stride, sizes that do not fit together, an output that overlaps an input,
  *    a workspace that is too small), UNSUPPORTED (a size beyond the kernels),

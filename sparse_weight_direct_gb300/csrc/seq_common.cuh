@@ -23,8 +23,8 @@ namespace seq {
 
 constexpr int kSMs = 152;
 constexpr int kVec = 8;  // positions a thread holds of a row
-constexpr int kMaxLength = 0x7fff0000;  // positions of a sequence: a block's reach beyond stays
-                                        // within 32 bits
+constexpr int kMaxLength = 0x7fff0000;  // positions, sequences, channels: a block's reach, or a
+                                        // grid's step (at most 65535), beyond stays within 32 bits
 
 // ---------------------------------------------------------------- elements
 

@@ -524,7 +524,8 @@ int check_sizes(const spconv_short_conv_args *a) {
     if (!a || a->N < 0 || a->C < 0 || a->L < 0 || a->K < 1) return SPCONV_ERR_INVALID_ARG;
     if (a->dtype < SPCONV_F32 || a->dtype > SPCONV_F16 || (a->silu & ~1))
         return SPCONV_ERR_INVALID_ARG;
-    if (a->K > 4 || a->L > kMaxLength) return SPCONV_ERR_UNSUPPORTED;
+    if (a->K > 4 || a->L > kMaxLength || a->N > kMaxLength || a->C > kMaxLength)
+        return SPCONV_ERR_UNSUPPORTED;
     if (!stride_ok(a->x_stride_n) || !stride_ok(a->x_stride_c) || !stride_ok(a->dy_stride_n) ||
         !stride_ok(a->dy_stride_c))
         return SPCONV_ERR_INVALID_ARG;

@@ -528,7 +528,8 @@ int scan_check_sizes(const spconv_scan_args *a) {
                       a->z_stride_n, a->z_stride_c, a->dy_stride_n, a->dy_stride_c, a->b_stride_n,
                       a->b_stride_g, a->b_stride_s, a->c_stride_n, a->c_stride_g, a->c_stride_s})
         if (!stride_ok(s)) return SPCONV_ERR_INVALID_ARG;
-    return a->S > 64 || a->L > kMaxLength ? SPCONV_ERR_UNSUPPORTED : SPCONV_OK;
+    return a->S > 64 || a->L > kMaxLength || a->channels > kMaxLength ? SPCONV_ERR_UNSUPPORTED
+                                                                      : SPCONV_OK;
 }
 
 ScanParams scan_params(const spconv_scan_args *a) {

@@ -308,3 +308,20 @@ def test_conv_without_positions_needs_its_weight():
     is refused, with or without positions."""
     assert refused("spconv_short_conv", conv_args(L=0, weight=None)) == _lib.SPCONV_ERR_INVALID_ARG
     assert refused("spconv_short_conv", conv_args(L=0, weight=None, final_state=None)) == _lib.SPCONV_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name,make,change", [
+    ("spconv_short_conv", conv_args, dict(N=0x7fffffff, C=1, L=1)),
+    ("spconv_short_conv", conv_args, dict(N=0x7fff0001, C=1, L=1)),
+    ("spconv_short_conv", conv_args, dict(N=1, C=0x7fffffff, L=1)),
+    ("spconv_short_conv_backward", conv_args, dict(N=0x7fffffff, C=1, L=1)),
+    ("spconv_short_conv_backward", conv_args, dict(N=1, C=0x7fffffff, L=1)),
+    ("spconv_short_conv_step", conv_args, dict(N=1, C=0x7fffffff, num_slots=1, x_stride_c=1)),
+    ("spconv_scan", scan_args, dict(N=1, channels=0x7fffffff, groups=1, L=1)),
+    ("spconv_scan_backward", scan_args, dict(N=1, channels=0x7fffffff, groups=1, L=1)),
+    ("spconv_scan_step", scan_args, dict(N=1, channels=0x7fffffff, groups=1, num_slots=1, u_stride_c=1,
+                                         delta_stride_c=1, z_stride_c=1, b_stride_s=1, c_stride_s=1)),
+])
+def test_sizes_near_2_to_the_31_are_refused(name, make, change):
+    """Counts of sequences and channels that a block's reach would take past 32 bits."""
+    assert refused(name, make(**change)) == _lib.SPCONV_ERR_UNSUPPORTED
