@@ -624,9 +624,19 @@ SPCONV_API int spconv_scan_backward(const spconv_scan_args *a, void *stream) {
     const int st = scan_check_sizes(a);
     if (st) return st;
     if (a->N > 65535) return SPCONV_ERR_UNSUPPORTED;  // sequences go along grid y
-    if (a->channels == 0) return SPCONV_OK;
     const int64_t rows = (int64_t)a->N * a->channels, L = a->L;
     const size_t e = dtype_size(a->dtype);
+    const int64_t bcb = (int64_t)a->N * a->groups * a->S * L * e;
+    if (a->channels == 0) {  // dB and dC are sums over no channel
+        if (bcb == 0) return SPCONV_OK;
+        if (!a->dB || !a->dC || !aligned(a->dB, e) || !aligned(a->dC, e) ||
+            overlap(a->dB, bcb, a->dC, bcb))
+            return SPCONV_ERR_INVALID_ARG;
+        const bool ok = cudaMemsetAsync(a->dB, 0, bcb, static_cast<cudaStream_t>(stream)) == cudaSuccess &&
+                        cudaMemsetAsync(a->dC, 0, bcb, static_cast<cudaStream_t>(stream)) == cudaSuccess;
+        if (!ok) cudaGetLastError();
+        return ok ? SPCONV_OK : SPCONV_ERR_CUDA;
+    }
     const bool any = rows > 0 && L > 0;
     if (!a->A || !a->dA) return SPCONV_ERR_INVALID_ARG;
     if (any && (!a->u || !a->delta || !a->B || !a->C || !a->dy || !a->du || !a->ddelta || !a->dB ||
@@ -644,7 +654,7 @@ SPCONV_API int spconv_scan_backward(const spconv_scan_args *a, void *stream) {
     const int64_t need = spconv_scan_backward_workspace(a);
     if (need && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need))
         return SPCONV_ERR_INVALID_ARG;
-    const int64_t act = rows * L * e, sb = rows * a->S * 4, bcb = (int64_t)a->N * a->groups * a->S * L * e;
+    const int64_t act = rows * L * e, sb = rows * a->S * 4;
     using Span = std::pair<const void *, int64_t>;
     const Span in[] = {
         {a->u, extent(a->N, a->channels, L, a->u_stride_n, a->u_stride_c, e)},

@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 import sequence_reference as ref  # noqa: E402
 import sparse_weight_direct_gb300 as swd  # noqa: E402
 from sparse_weight_direct_gb300 import _lib  # noqa: E402
-from test_sequence import F32, TYPE_IDS, TYPES, Draw, adapter_args, conv_args, scan_args  # noqa: E402
+from test_sequence import F32, GOOD, TYPE_IDS, TYPES, Draw, adapter_args, conv_args, scan_args  # noqa: E402
 
 # ------------------------------------------------------------------ adapters: sums of very different size
 
@@ -325,3 +325,26 @@ def test_conv_without_positions_needs_its_weight():
 def test_sizes_near_2_to_the_31_are_refused(name, make, change):
     """Counts of sequences and channels that a block's reach would take past 32 bits."""
     assert refused(name, make(**change)) == _lib.SPCONV_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ no channels
+
+
+def test_gradients_of_no_channels_need_their_outputs():
+    """dB and dC have elements without any channel: sums over none."""
+    for change in (dict(dB=None), dict(dC=None), dict(dB=GOOD + 2)):
+        assert refused("spconv_scan_backward", scan_args(channels=0, **change)) == _lib.SPCONV_ERR_INVALID_ARG
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("groups", [None, 1, 3])
+@pytest.mark.parametrize("dtype", TYPES, ids=TYPE_IDS)
+def test_gradients_of_no_channels_are_zero(dtype, groups):
+    N, L, S = 2, 7, 16
+    x, A = torch.zeros(N, 0, L, dtype=dtype, device="cuda"), torch.zeros(0, S, device="cuda")
+    B = torch.ones(*((N, S, L) if groups is None else (N, groups, S, L)), dtype=dtype, device="cuda")
+    junk = [torch.full_like(B, float("nan")) for _ in range(4)]  # what the outputs' memory holds
+    torch.cuda.synchronize()
+    del junk
+    g = swd.scan_backward(x, x, x, A, B, B)
+    assert g["dB"].shape == B.shape and not g["dB"].any() and not g["dC"].any()
