@@ -810,8 +810,9 @@ SPCONV_API int spconv_adapter_add(const spconv_adapter_args *a, void *stream) {
     if (!aligned(a->index, 4) || !aligned(a->scale, 4)) return SPCONV_ERR_INVALID_ARG;
     const int64_t ab = (int64_t)a->adapters * a->R * e;
     if ((a->out != a->y && overlap(a->out, out * e, a->y, out * e)) ||
-        overlap(a->out, out * e, a->x, extent(a->N, a->C, a->P, a->x_stride_n, a->x_stride_c, e)) ||
-        overlap(a->out, out * e, a->a, ab * a->C) || overlap(a->out, out * e, a->b, ab * a->M))
+        !apart({{a->out, (int64_t)(out * e)}},
+               {{a->x, extent(a->N, a->C, a->P, a->x_stride_n, a->x_stride_c, e)}, {a->a, ab * a->C},
+                {a->b, ab * a->M}, {a->index, a->N * 4LL}, {a->scale, a->adapters * 4LL}}))
         return SPCONV_ERR_INVALID_ARG;
     AdapterParams p{};
     p.x = a->x; p.a = a->a; p.b = a->b; p.y = a->y; p.index = a->index; p.scale = a->scale;

@@ -234,6 +234,22 @@ inline bool overlap(const void *a, int64_t an, const void *b, int64_t bn) {
     return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
 
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// No output lies over another one or over what is read.
+inline bool apart(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+    for (const Span &o : out) {
+        for (const Span &i : in)
+            if (overlap(o.p, o.bytes, i.p, i.bytes)) return false;
+        for (const Span *k = out.begin(); k != &o; ++k)
+            if (overlap(o.p, o.bytes, k->p, k->bytes)) return false;
+    }
+    return true;
+}
+
 // A stride that 64-bit byte offsets can hold for any valid index.
 inline bool stride_ok(int64_t s) { return s >= 0 && s <= (int64_t)1 << 40; }
 

@@ -566,6 +566,9 @@ bool on_elements(const spconv_short_conv_args *a, std::initializer_list<const vo
     return true;
 }
 
+Span weights_of(const spconv_short_conv_args *a) { return {a->weight, (int64_t)a->C * a->K * 4}; }
+Span bias_of(const spconv_short_conv_args *a) { return {a->bias, a->C * 4LL}; }
+
 bool on_words(std::initializer_list<const void *> ps) {
     for (const void *q : ps)
         if (q && !aligned(q, 4)) return false;
@@ -590,9 +593,8 @@ SPCONV_API int spconv_short_conv(const spconv_short_conv_args *a, void *stream) 
         return SPCONV_ERR_INVALID_ARG;
     const int64_t xb = extent(a->N, a->C, a->L, a->x_stride_n, a->x_stride_c, e);
     const int64_t yb = rows * a->L * e, sb = rows * (a->K - 1) * e;
-    if (overlap(a->x, xb, a->y, yb) || overlap(a->x, xb, a->final_state, sb) ||
-        overlap(a->state, sb, a->final_state, sb) || overlap(a->state, sb, a->y, yb) ||
-        overlap(a->y, yb, a->final_state, sb))
+    if (!apart({{a->y, yb}, {a->final_state, sb}},
+               {{a->x, xb}, {a->state, sb}, weights_of(a), bias_of(a), {a->lengths, a->N * 4LL}}))
         return SPCONV_ERR_INVALID_ARG;
     ConvParams p = params_of(a);
     p.vec_y = rows_aligned(a->y, 0, a->L, e);
@@ -640,11 +642,10 @@ SPCONV_API int spconv_short_conv_backward(const spconv_short_conv_args *a, void 
     const int64_t xb = extent(a->N, a->C, a->L, a->x_stride_n, a->x_stride_c, e);
     const int64_t db = extent(a->N, a->C, a->L, a->dy_stride_n, a->dy_stride_c, e);
     const int64_t yb = rows * a->L * e, sb = rows * (a->K - 1) * e;
-    if (overlap(a->x, xb, a->dx, yb) || overlap(a->dy, db, a->dx, yb) ||
-        overlap(a->state, sb, a->dx, yb) || overlap(a->dfinal_state, sb, a->dx, yb) ||
-        overlap(a->x, xb, a->dstate, sb) || overlap(a->dy, db, a->dstate, sb) ||
-        overlap(a->state, sb, a->dstate, sb) || overlap(a->dfinal_state, sb, a->dstate, sb) ||
-        overlap(a->dx, yb, a->dstate, sb))
+    if (!apart({{a->dx, yb}, {a->dstate, sb}, {a->dweight, weights_of(a).bytes},
+                {a->dbias, bias_of(a).bytes}, {a->workspace, need}},
+               {{a->x, xb}, {a->dy, db}, {a->state, sb}, {a->dfinal_state, sb}, weights_of(a),
+                bias_of(a), {a->lengths, a->N * 4LL}}))
         return SPCONV_ERR_INVALID_ARG;
     ConvParams p = params_of(a);
     p.vec_y = rows_aligned(a->dx, 0, a->L, e);
@@ -685,8 +686,8 @@ SPCONV_API int spconv_short_conv_step(const spconv_short_conv_args *a, void *str
         return SPCONV_ERR_INVALID_ARG;
     const int64_t xb = extent(a->N, a->C, 1, a->x_stride_n, 1, e), yb = rows * e;
     const int64_t sb = (int64_t)a->num_slots * a->C * (a->K - 1) * e;
-    if (overlap(a->x, xb, a->y, yb) || overlap(a->x, xb, a->pool, sb) ||
-        overlap(a->y, yb, a->pool, sb))
+    if (!apart({{a->y, yb}, {a->pool, sb}},
+               {{a->x, xb}, weights_of(a), bias_of(a), {a->slots, a->N * 4LL}}))
         return SPCONV_ERR_INVALID_ARG;
     const ConvParams p = params_of(a);
     const dim3 grid((unsigned)((a->C - 1) / kThreads + 1), a->N);

@@ -635,13 +635,17 @@ int64_t state_floats(const ScanParams &p) {
     return ((int64_t)p.N * p.chunks * p.channels * p.S + 3) / 4 * 4;
 }
 
+int64_t workspace_bytes(const ScanParams &p) {
+    return p.chunks == 1 ? 0 : (state_floats(p) + (int64_t)p.N * p.chunks * p.channels) * 4;
+}
+
 }  // namespace
 
 SPCONV_API int64_t spconv_scan_workspace(const spconv_scan_args *a) {
     if (scan_check_sizes(a) || a->channels == 0 || a->N == 0) return 0;
     ScanParams p = scan_params(a);
     plan_chunks(p);
-    return p.chunks == 1 ? 0 : (state_floats(p) + (int64_t)p.N * p.chunks * p.channels) * 4;
+    return workspace_bytes(p);
 }
 
 SPCONV_API int spconv_scan(const spconv_scan_args *a, void *stream) {
@@ -657,22 +661,19 @@ SPCONV_API int spconv_scan(const spconv_scan_args *a, void *stream) {
         !words({a->A, a->D, a->delta_bias, a->state, a->lengths, a->final_state}))
         return SPCONV_ERR_INVALID_ARG;
     const int64_t L = a->L, yb = rows * L * e, sb = rows * a->S * 4;
-    const int64_t bb = extent(a->N, a->groups, (a->S - 1) * a->b_stride_s + L, a->b_stride_n, a->b_stride_g, e);
-    const int64_t cb = extent(a->N, a->groups, (a->S - 1) * a->c_stride_s + L, a->c_stride_n, a->c_stride_g, e);
-    if (L > 0)
-        for (const auto &o : {std::pair<const void *, int64_t>{a->y, yb}, {a->final_state, sb}})
-            if (overlap(o.first, o.second, a->u, extent(a->N, a->channels, L, a->u_stride_n, a->u_stride_c, e)) ||
-                overlap(o.first, o.second, a->delta, extent(a->N, a->channels, L, a->delta_stride_n, a->delta_stride_c, e)) ||
-                overlap(o.first, o.second, a->z, extent(a->N, a->channels, L, a->z_stride_n, a->z_stride_c, e)) ||
-                overlap(o.first, o.second, a->B, bb) || overlap(o.first, o.second, a->C, cb) ||
-                overlap(o.first, o.second, a->state, sb))
-                return SPCONV_ERR_INVALID_ARG;
-    if (overlap(a->y, yb, a->final_state, sb) || overlap(a->state, sb, a->final_state, sb))
-        return SPCONV_ERR_INVALID_ARG;
     ScanParams p = scan_params(a);
     plan_chunks(p);
-    if (p.chunks > 1) {
-        const int64_t need = spconv_scan_workspace(a);
+    const int64_t need = workspace_bytes(p);
+    const int64_t bb = L ? extent(a->N, a->groups, (a->S - 1) * a->b_stride_s + L, a->b_stride_n, a->b_stride_g, e) : 0;
+    const int64_t cb = L ? extent(a->N, a->groups, (a->S - 1) * a->c_stride_s + L, a->c_stride_n, a->c_stride_g, e) : 0;
+    if (!apart({{a->y, yb}, {a->final_state, sb}, {a->workspace, need}},
+               {{a->u, extent(a->N, a->channels, L, a->u_stride_n, a->u_stride_c, e)},
+                {a->delta, extent(a->N, a->channels, L, a->delta_stride_n, a->delta_stride_c, e)},
+                {a->z, extent(a->N, a->channels, L, a->z_stride_n, a->z_stride_c, e)},
+                {a->B, bb}, {a->C, cb}, {a->state, sb}, {a->lengths, a->N * 4LL},
+                {a->A, a->channels * 4LL * a->S}, {a->D, a->channels * 4LL}, {a->delta_bias, a->channels * 4LL}}))
+        return SPCONV_ERR_INVALID_ARG;
+    if (need) {
         if (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need)
             return SPCONV_ERR_INVALID_ARG;
         p.h_chunk = static_cast<float *>(a->workspace);
@@ -718,14 +719,15 @@ SPCONV_API int spconv_scan_step(const spconv_scan_args *a, void *stream) {
         !words({a->A, a->D, a->delta_bias, a->pool, a->slots}))
         return SPCONV_ERR_INVALID_ARG;
     const int64_t yb = rows * e, sb = (int64_t)a->num_slots * a->channels * a->S * 4;
-    for (const auto &o : {std::pair<const void *, int64_t>{a->y, yb}, {a->pool, sb}})
-        if (overlap(o.first, o.second, a->u, extent(a->N, a->channels, 1, a->u_stride_n, 1, e)) ||
-            overlap(o.first, o.second, a->delta, extent(a->N, a->channels, 1, a->delta_stride_n, 1, e)) ||
-            overlap(o.first, o.second, a->z, extent(a->N, a->channels, 1, a->z_stride_n, 1, e)) ||
-            overlap(o.first, o.second, a->B, extent(a->N, a->groups, a->S, a->b_stride_n, a->b_stride_g, e)) ||
-            overlap(o.first, o.second, a->C, extent(a->N, a->groups, a->S, a->c_stride_n, a->c_stride_g, e)))
-            return SPCONV_ERR_INVALID_ARG;
-    if (overlap(a->y, yb, a->pool, sb)) return SPCONV_ERR_INVALID_ARG;
+    if (!apart({{a->y, yb}, {a->pool, sb}},
+               {{a->u, extent(a->N, a->channels, 1, a->u_stride_n, 1, e)},
+                {a->delta, extent(a->N, a->channels, 1, a->delta_stride_n, 1, e)},
+                {a->z, extent(a->N, a->channels, 1, a->z_stride_n, 1, e)},
+                {a->B, extent(a->N, a->groups, a->S, a->b_stride_n, a->b_stride_g, e)},
+                {a->C, extent(a->N, a->groups, a->S, a->c_stride_n, a->c_stride_g, e)},
+                {a->A, a->channels * 4LL * a->S}, {a->D, a->channels * 4LL}, {a->delta_bias, a->channels * 4LL},
+                {a->slots, a->N * 4LL}}))
+        return SPCONV_ERR_INVALID_ARG;
     ScanParams p = scan_params(a);
     p.vec = aligned(a->pool, 16) && aligned(a->A, 16) &&
             rows_aligned(a->B, a->b_stride_n, a->b_stride_g, e) &&

@@ -655,24 +655,18 @@ SPCONV_API int spconv_scan_backward(const spconv_scan_args *a, void *stream) {
     if (need && (!a->workspace || !aligned(a->workspace, 16) || a->workspace_bytes < need))
         return SPCONV_ERR_INVALID_ARG;
     const int64_t act = rows * L * e, sb = rows * a->S * 4;
-    using Span = std::pair<const void *, int64_t>;
-    const Span in[] = {
-        {a->u, extent(a->N, a->channels, L, a->u_stride_n, a->u_stride_c, e)},
-        {a->delta, extent(a->N, a->channels, L, a->delta_stride_n, a->delta_stride_c, e)},
-        {a->z, extent(a->N, a->channels, L, a->z_stride_n, a->z_stride_c, e)},
-        {a->dy, extent(a->N, a->channels, L, a->dy_stride_n, a->dy_stride_c, e)},
-        {a->B, extent(a->N, a->groups, (a->S - 1) * a->b_stride_s + L, a->b_stride_n, a->b_stride_g, e)},
-        {a->C, extent(a->N, a->groups, (a->S - 1) * a->c_stride_s + L, a->c_stride_n, a->c_stride_g, e)},
-        {a->state, sb},
-        {a->dfinal_state, sb}};
-    const Span out[] = {{a->du, act}, {a->ddelta, act}, {a->dz, act}, {a->dB, bcb}, {a->dC, bcb}, {a->dstate, sb}};
-    for (const Span &o : out)
-        for (const Span &i : in)
-            if (overlap(o.first, o.second, i.first, i.second)) return SPCONV_ERR_INVALID_ARG;
-    for (int i = 0; i < 6; ++i)
-        for (int k = 0; k < i; ++k)
-            if (overlap(out[i].first, out[i].second, out[k].first, out[k].second))
-                return SPCONV_ERR_INVALID_ARG;
+    const int64_t bb = L ? extent(a->N, a->groups, (a->S - 1) * a->b_stride_s + L, a->b_stride_n, a->b_stride_g, e) : 0;
+    const int64_t cb = L ? extent(a->N, a->groups, (a->S - 1) * a->c_stride_s + L, a->c_stride_n, a->c_stride_g, e) : 0;
+    const int64_t ab = a->channels * 4LL * a->S, per = a->channels * 4LL;
+    if (!apart({{a->du, act}, {a->ddelta, act}, {a->dz, act}, {a->dB, bcb}, {a->dC, bcb}, {a->dstate, sb},
+                {a->dA, ab}, {a->dD, per}, {a->ddelta_bias, per}, {a->workspace, need}},
+               {{a->u, extent(a->N, a->channels, L, a->u_stride_n, a->u_stride_c, e)},
+                {a->delta, extent(a->N, a->channels, L, a->delta_stride_n, a->delta_stride_c, e)},
+                {a->z, extent(a->N, a->channels, L, a->z_stride_n, a->z_stride_c, e)},
+                {a->dy, extent(a->N, a->channels, L, a->dy_stride_n, a->dy_stride_c, e)},
+                {a->B, bb}, {a->C, cb}, {a->state, sb}, {a->dfinal_state, sb}, {a->lengths, a->N * 4LL},
+                {a->A, ab}, {a->D, per}, {a->delta_bias, per}}))
+        return SPCONV_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     ScanParams p = scan_params(a);
     if (!any) {

@@ -348,3 +348,41 @@ def test_gradients_of_no_channels_are_zero(dtype, groups):
     del junk
     g = swd.scan_backward(x, x, x, A, B, B)
     assert g["dB"].shape == B.shape and not g["dB"].any() and not g["dC"].any()
+
+
+# ------------------------------------------------------------------ outputs over what a call reads
+
+STEP = dict(num_slots=2, u_stride_c=1, delta_stride_c=1, z_stride_c=1, b_stride_s=1, c_stride_s=1)
+READ_AND_WRITTEN = [
+    ("spconv_short_conv", conv_args, {}, "y final_state", "x weight bias state lengths"),
+    ("spconv_short_conv_backward", conv_args, {}, "dx dstate dweight dbias",
+     "x weight bias state lengths dy dfinal_state"),
+    ("spconv_short_conv_backward", conv_args, dict(N=4096, L=4096, workspace_bytes=1 << 30),
+     "dx dstate dweight dbias workspace", "x weight bias state dy dfinal_state"),
+    ("spconv_short_conv_step", conv_args, dict(num_slots=2, x_stride_c=1), "y pool", "x weight bias slots"),
+    ("spconv_scan", scan_args, {}, "y final_state", "u delta z B C A D delta_bias state lengths"),
+    ("spconv_scan", scan_args, dict(N=1, L=4096, workspace_bytes=1 << 30), "y final_state workspace",
+     "u delta z B C A D delta_bias state"),
+    ("spconv_scan_backward", scan_args, {},
+     "du ddelta dz dB dC dA dD ddelta_bias dstate workspace",
+     "u delta z B C A D delta_bias state lengths dy dfinal_state"),
+    ("spconv_scan_step", scan_args, STEP, "y pool", "u delta z B C A D delta_bias slots"),
+    ("spconv_adapter_add", adapter_args, {}, "out", "x a b index scale"),
+]
+
+
+@pytest.mark.parametrize("name,make,change,out,read", READ_AND_WRITTEN,
+                         ids=[f"{n[7:]}-{i}" for i, (n, *_) in enumerate(READ_AND_WRITTEN)])
+def test_outputs_over_inputs_are_refused(name, make, change, out, read):
+    """Every output that lies over an input or over another output: all pointers
+    a gigabyte apart but for the two."""
+    fields = [f for f, t in make()._fields_ if t is ctypes.c_void_p]
+    far = {f: (1 << 40) + (i << 34) for i, f in enumerate(fields)}
+    given = {f: far[f] if f in (out + " " + read).split() else None for f in fields}
+    if name == "spconv_adapter_add":
+        given["y"] = far["y"]  # (out may be y itself)
+    for o in out.split():
+        for other in (out + " " + read).split():
+            if o != other:
+                args = make(**{**change, **given, o: far[other]})
+                assert refused(name, args) == _lib.SPCONV_ERR_INVALID_ARG, (o, other)
