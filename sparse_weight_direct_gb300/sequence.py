@@ -52,12 +52,18 @@ def _fail(what):
     raise SpconvError(_lib.SPCONV_ERR_INVALID_ARG, what)
 
 
+def _not_packed(error):
+    _fail(f"a size or a flag of the call does not fit its 32 bits ({error})")
+
+
 def _begin(t, name, dims):
     """The tensor that a call's others go by: its type, its code, its device."""
     if _torch is None:
         _load()
     if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype not in _codes or t.dim() != dims:
         _fail(f"{name} must be a float32, bfloat16 or float16 CUDA tensor with {dims} dimensions")
+    if t.numel() >> 31 and max(t.shape) >> 31:  # (before anything of that size is allocated)
+        _fail(f"{name} has a size that is not below 2^31")
     dtype, device = t.dtype, t.get_device()
     if device != _current_device():
         _fail(f"{name} must be on the current CUDA device")
@@ -159,11 +165,14 @@ def short_conv(x, weight, bias=None, *, silu: bool = True, state=None, final_sta
     x_at, (xn, xc, _) = _rows(x, "x", dt, dev, shape)
     if out is None:
         out = _like(x)
-    args = _pack_conv(
-        N, C, L, K, code, silu, 0, 0, xn, xc, 0, 0, x_at, _whole(weight, "weight", _f32, dev, (C, K)),
-        _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
-        _whole(lengths, "lengths", _i32, dev, (N,)), 0, _whole(out, "out", dt, dev, shape),
-        _whole(final_state, "final_state", dt, dev, st), 0, 0, 0, 0, 0, 0, 0)
+    try:
+        args = _pack_conv(
+            N, C, L, K, code, silu, 0, 0, xn, xc, 0, 0, x_at, _whole(weight, "weight", _f32, dev, (C, K)),
+            _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
+            _whole(lengths, "lengths", _i32, dev, (N,)), 0, _whole(out, "out", dt, dev, shape),
+            _whole(final_state, "final_state", dt, dev, st), 0, 0, 0, 0, 0, 0, 0)
+    except struct.error as error:
+        _not_packed(error)
     _run(_library.spconv_short_conv, args + _no_workspace, dev)
     return out
 
@@ -185,12 +194,15 @@ def short_conv_backward(dy, x, weight, bias=None, *, silu: bool = True, state=No
     dx, dw = _new(shape, dt, dev), _new((C, K), _f32, dev)
     db = _new((C,), _f32, dev) if bias is not None else None
     ds = _new(st, dt, dev) if state is not None else None
-    args = _pack_conv(
-        N, C, L, K, code, silu, 0, 0, xn, xc, dyn, dyc, x_at, _whole(weight, "weight", _f32, dev, (C, K)),
-        _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
-        _whole(lengths, "lengths", _i32, dev, (N,)), 0, 0, 0, 0, dy_at,
-        _whole(dfinal_state, "dfinal_state", dt, dev, st), dx.data_ptr(),
-        0 if ds is None else ds.data_ptr(), dw.data_ptr(), 0 if db is None else db.data_ptr())
+    try:
+        args = _pack_conv(
+            N, C, L, K, code, silu, 0, 0, xn, xc, dyn, dyc, x_at, _whole(weight, "weight", _f32, dev, (C, K)),
+            _whole(bias, "bias", _f32, dev, (C,)), _whole(state, "state", dt, dev, st),
+            _whole(lengths, "lengths", _i32, dev, (N,)), 0, 0, 0, 0, dy_at,
+            _whole(dfinal_state, "dfinal_state", dt, dev, st), dx.data_ptr(),
+            0 if ds is None else ds.data_ptr(), dw.data_ptr(), 0 if db is None else db.data_ptr())
+    except struct.error as error:
+        _not_packed(error)
     _run(_library.spconv_short_conv_backward, args, dev,
          _library.spconv_short_conv_backward_workspace)
     return dx, dw, db, ds
@@ -212,10 +224,13 @@ def short_conv_step(x, state, weight, bias=None, *, silu: bool = True, slots=Non
     x_at, (xn, _) = _rows(x, "x", dt, dev, shape)
     if out is None:
         out = _like(x)
-    args = _pack_conv(
-        N, C, 1, K, code, silu, pool, 0, xn, 1, 0, 0, x_at, _whole(weight, "weight", _f32, dev, (C, K)), _whole(bias, "bias", _f32, dev, (C,)), 0, 0,
-        _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape), 0,
-        _whole(state, "state", dt, dev, (pool, C, K - 1)), 0, 0, 0, 0, 0, 0)
+    try:
+        args = _pack_conv(
+            N, C, 1, K, code, silu, pool, 0, xn, 1, 0, 0, x_at, _whole(weight, "weight", _f32, dev, (C, K)), _whole(bias, "bias", _f32, dev, (C,)), 0, 0,
+            _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape), 0,
+            _whole(state, "state", dt, dev, (pool, C, K - 1)), 0, 0, 0, 0, 0, 0)
+    except struct.error as error:
+        _not_packed(error)
     _run(_library.spconv_short_conv_step, args + _no_workspace, dev)
     return out
 
@@ -276,10 +291,13 @@ def scan(u, delta, A, B, C, D=None, z=None, delta_bias=None, *, softplus: bool =
     states = (shape[0], shape[1], S)
     if out is None:
         out = _like(u)
-    args = _pack_scan(
-        *given, _whole(state, "state", _f32, dev, states),
-        _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, _whole(out, "out", dt, dev, shape),
-        _whole(final_state, "final_state", _f32, dev, states), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    try:
+        args = _pack_scan(
+            *given, _whole(state, "state", _f32, dev, states),
+            _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, _whole(out, "out", dt, dev, shape),
+            _whole(final_state, "final_state", _f32, dev, states), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    except struct.error as error:
+        _not_packed(error)
     _run(_library.spconv_scan, args, dev,
          _library.spconv_scan_workspace)
     return out
@@ -307,11 +325,14 @@ def scan_backward(dy, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, sof
              ddelta_bias=None if delta_bias is None else _new(delta_bias.shape, _f32, dev),
              dstate=None if state is None else _new(states, _f32, dev))
     at = {k: 0 if t is None else t.data_ptr() for k, t in g.items()}
-    args = _pack_scan(
-        *given, _whole(state, "state", _f32, dev, states),
-        _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, 0, 0, 0, dy_at,
-        _whole(dfinal_state, "dfinal_state", _f32, dev, states), at["du"], at["ddelta"], at["dz"],
-        at["dB"], at["dC"], at["dA"], at["dD"], at["ddelta_bias"], at["dstate"])
+    try:
+        args = _pack_scan(
+            *given, _whole(state, "state", _f32, dev, states),
+            _whole(lengths, "lengths", _i32, dev, shape[:1]), 0, 0, 0, 0, dy_at,
+            _whole(dfinal_state, "dfinal_state", _f32, dev, states), at["du"], at["ddelta"], at["dz"],
+            at["dB"], at["dC"], at["dA"], at["dD"], at["ddelta_bias"], at["dstate"])
+    except struct.error as error:
+        _not_packed(error)
     _run(_library.spconv_scan_backward, args, dev,
          _library.spconv_scan_backward_workspace)
     return g
@@ -332,9 +353,12 @@ def scan_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, *, soft
     given, S, _ = _scan_inputs(dt, code, dev, u, delta, A, B, C, D, z, delta_bias, softplus, True, pool)
     if out is None:
         out = _like(u)
-    args = _pack_scan(
-        *given, 0, 0, _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape),
-        0, _whole(state, "state", _f32, dev, (pool, ch, S)), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    try:
+        args = _pack_scan(
+            *given, 0, 0, _whole(slots, "slots", _i32, dev, (N,)), _whole(out, "out", dt, dev, shape),
+            0, _whole(state, "state", _f32, dev, (pool, ch, S)), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    except struct.error as error:
+        _not_packed(error)
     _run(_library.spconv_scan_step, args + _no_workspace, dev)
     return out
 
@@ -361,9 +385,12 @@ def adapter_add(y, x, a, b, index, *, scale=None, out=None, stream=None):
     x_at, xs = _rows(x, "x", dt, dev, x.shape)
     if out is None:
         out = _like(y)
-    args = _pack_adapter(
-        N, P, C, M, R, K, code, 0, xs[0], xs[1], x_at, _whole(a, "a", dt, dev, (K, R, C)), _whole(b, "b", dt, dev, (K, M, R)),
-        _whole(index, "index", _i32, dev, (N,)), _whole(scale, "scale", _f32, dev, (K,)), y_at,
-        _whole(out, "out", dt, dev, shape))
+    try:
+        args = _pack_adapter(
+            N, P, C, M, R, K, code, 0, xs[0], xs[1], x_at, _whole(a, "a", dt, dev, (K, R, C)), _whole(b, "b", dt, dev, (K, M, R)),
+            _whole(index, "index", _i32, dev, (N,)), _whole(scale, "scale", _f32, dev, (K,)), y_at,
+            _whole(out, "out", dt, dev, shape))
+    except struct.error as error:
+        _not_packed(error)
     _run(_library.spconv_adapter_add, args, dev)
     return out

@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 import sequence_reference as ref  # noqa: E402
 import sparse_weight_direct_gb300 as swd  # noqa: E402
 from sparse_weight_direct_gb300 import _lib  # noqa: E402
-from test_sequence import F32, GOOD, TYPE_IDS, TYPES, Draw, adapter_args, conv_args, scan_args  # noqa: E402
+from test_sequence import BF16, F32, GOOD, TYPE_IDS, TYPES, Draw, adapter_args, conv_args, scan_args  # noqa: E402
 
 # ------------------------------------------------------------------ adapters: sums of very different size
 
@@ -386,3 +386,38 @@ def test_outputs_over_inputs_are_refused(name, make, change, out, read):
             if o != other:
                 args = make(**{**change, **given, o: far[other]})
                 assert refused(name, args) == _lib.SPCONV_ERR_INVALID_ARG, (o, other)
+
+
+# ------------------------------------------------------------------ refusals at the Python entry
+
+
+@pytest.mark.gpu
+def test_sizes_past_32_bits_are_refused():
+    """Views of one element with 2^31 of them along a dimension, a pool of 2^31
+    states, and flags that are none: SpconvError, and nothing is allocated."""
+    many = 1 << 31
+    one = torch.zeros(1, device="cuda")
+    wide = lambda *shape: one.as_strided(shape, (0,) * len(shape))  # noqa: E731
+    w, A = torch.zeros(1, 2, device="cuda"), torch.zeros(1, 1, device="cuda")
+    bf, x = torch.zeros(1, 1, 1, dtype=BF16, device="cuda"), torch.zeros(1, 1, 1, device="cuda")
+    pool = torch.empty(many, 1, 1, dtype=BF16, device="cuda")  # 4 GB
+    index = torch.zeros(1, dtype=torch.int32, device="cuda")
+    calls = [
+        lambda: swd.short_conv(wide(many, 1, 1), w), lambda: swd.short_conv(wide(1, many, 1), w),
+        lambda: swd.short_conv_backward(wide(many, 1, 1), wide(many, 1, 1), w),
+        lambda: swd.short_conv_step(wide(many, 1), x, w),
+        lambda: swd.short_conv_step(bf[..., 0], pool, w, slots=index),
+        lambda: swd.scan(wide(many, 1, 1), wide(many, 1, 1), A, wide(many, 1, 1), wide(many, 1, 1)),
+        lambda: swd.scan_backward(*[wide(many, 1, 1)] * 3, A, *[wide(many, 1, 1)] * 2),
+        lambda: swd.scan_step(x, wide(many, 1), wide(many, 1), A, wide(many, 1), wide(many, 1)),
+        lambda: swd.adapter_add(x, wide(1, many, 1), x, x, index),
+        lambda: swd.short_conv(x, w, silu=1 << 40), lambda: swd.scan(x, x, A, x, x, softplus="no"),
+    ]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    for i, call in enumerate(calls):
+        with pytest.raises(swd.SpconvError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    assert torch.cuda.max_memory_allocated() - before < 1 << 20
