@@ -22,12 +22,18 @@ import struct
 from . import _lib
 from ._lib import SpconvError
 
-# The argument structures of include/spconv.h without their last two members
-# (workspace, workspace_bytes), packed in one go: filling a ctypes structure
-# field by field costs more than a short kernel runs.
-_pack_conv = struct.Struct("8i4q15P").pack
-_pack_scan = struct.Struct("8i14q25P").pack
-_pack_adapter = struct.Struct("8i2q7P").pack
+_codes_of = {_lib._i32: "i", _lib._i64: "q", _lib._ptr: "P"}
+
+
+def _packer(structure):
+    """Packs an argument structure of include/spconv.h, all but the workspace and
+    its bytes, in one go: filling a ctypes structure field by field costs more
+    than a short kernel runs."""
+    return struct.Struct("".join(_codes_of[t] for n, t in structure._fields_ if "workspace" not in n)).pack
+
+
+_pack_conv, _pack_scan, _pack_adapter = (
+    _packer(s) for s in (_lib.ShortConvArgs, _lib.ScanArgs, _lib.AdapterArgs))
 _pack_workspace = struct.Struct("Pq").pack
 _no_workspace = _pack_workspace(0, 0)
 

@@ -421,3 +421,20 @@ def test_sizes_past_32_bits_are_refused():
             call()
             pytest.fail(f"call {i} was not refused")
     assert torch.cuda.max_memory_allocated() - before < 1 << 20
+
+
+def test_calls_pack_the_structures_of_the_header():
+    """What the Python calls pack is the structure that is compared with the
+    header, up to its workspace."""
+    from sparse_weight_direct_gb300 import sequence
+    for pack, structure in ((sequence._pack_conv, _lib.ShortConvArgs), (sequence._pack_scan, _lib.ScanArgs),
+                            (sequence._pack_adapter, _lib.AdapterArgs)):
+        names = [n for n, _ in structure._fields_ if "workspace" not in n]
+        packed = pack(*range(1, len(names) + 1))
+        if hasattr(structure, "workspace"):
+            packed += sequence._pack_workspace(1 << 40, 1 << 41)
+        assert len(packed) == ctypes.sizeof(structure)
+        read = structure.from_buffer_copy(packed)
+        assert [getattr(read, n) for n in names] == list(range(1, len(names) + 1))
+        if hasattr(structure, "workspace"):
+            assert (read.workspace, read.workspace_bytes) == (1 << 40, 1 << 41)
