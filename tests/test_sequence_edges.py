@@ -9,6 +9,7 @@ torch = pytest.importorskip("torch")
 
 import sequence_reference as ref  # noqa: E402
 import sparse_weight_direct_gb300 as swd  # noqa: E402
+import test_sequence as base  # noqa: E402
 from sparse_weight_direct_gb300 import _lib  # noqa: E402
 from test_sequence import BF16, F32, GOOD, TYPE_IDS, TYPES, Draw, adapter_args, conv_args, scan_args  # noqa: E402
 
@@ -438,3 +439,81 @@ def test_calls_pack_the_structures_of_the_header():
         assert [getattr(read, n) for n in names] == list(range(1, len(names) + 1))
         if hasattr(structure, "workspace"):
             assert (read.workspace, read.workspace_bytes) == (1 << 40, 1 << 41)
+
+
+# ------------------------------------------------------------------ sizes as served
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("case", [
+    # N, P, C, M, R, adapters: clusters of eight and four blocks, aligned and not
+    (2, 64, 512, 520, 16, 2), (2, 70, 256, 300, 32, 2), (2, 1, 1100, 600, 16, 2), (5, 1, 256, 300, 33, 2),
+    # more tiles of y for a warp than it has on their way, in one block and in eight
+    (1, 64, 40, 1040, 8, 1), (1, 128, 512, 8200, 48, 1),
+    # more rows of b than a block takes at a time
+    (3, 1, 512, 4200, 16, 2), (2, 1, 64, 1100, 64, 2),
+], ids=lambda c: "x".join(map(str, c)))
+def test_adapter_clusters_and_rounds(case, dtype):
+    base.test_adapter_add(case, dtype, False)
+    base.test_adapter_add(case, dtype, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("case", [(1, 40, 640, 64, 1), (1, 33, 300, 20, 1), (2, 20, 520, 33, 2), (8, 4, 600, 48, 2)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_scan_of_many_states_in_chunks(case, ragged, dtype):
+    """More than 16 states in sequences that are cut."""
+    N, ch, L, S, G = case
+    assert _lib.lib().spconv_scan_workspace(ctypes.byref(scan_args(N=N, channels=ch, L=L, S=S, groups=G))) > 0
+    base.test_scan(case, dtype, ragged, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("L", [40, 300, 1030])
+def test_a_padded_sequence_is_the_sequence_alone(dtype, L):
+    """Outputs, states and gradients of a sequence with NaN behind its end against
+    those of the sequence alone, wherever the end lies in a tile or a chunk.  The
+    gradients go by tiles and segments of fixed places here: bit for bit.  So does
+    the forward pass up to 127 positions; longer ones are cut into other chunks, so
+    that states are joined at other places."""
+    s, dy, state, dfinal, _ = base.scan_inputs((1, 40, L, 16, 1), dtype, False, seed=20)
+    rows = ("u", "delta", "B", "C", "z")
+    for k in (1, 7, 32, 33, L // 2 + 3, L - 1):
+        lens = torch.tensor([k], dtype=torch.int32, device="cuda")
+        far = {n: base.poison(v, lens) if n in rows else v for n, v in s.items()}
+        cut = {n: v[..., :k].contiguous() if n in rows else v for n, v in s.items()}
+        ends = torch.empty_like(state), torch.empty_like(state)
+        y = swd.scan(**far, state=state, final_state=ends[0], lengths=lens)
+        alone = swd.scan(**cut, state=state, final_state=ends[1])
+        assert not y[..., k:].any()
+        tight = 2.0 ** -19 if L >= 128 else 0.0
+        for a, b in ((y[..., :k], alone), ends):
+            a, b = a.double(), b.double()
+            unit = 2 * ref.HALF[dtype] * b.abs() if tight else 0.0
+            assert ((a - b).abs() <= tight * b.abs().max() + unit).all(), k
+        g = swd.scan_backward(base.poison(dy, lens), **far, state=state, dfinal_state=dfinal, lengths=lens)
+        h = swd.scan_backward(dy[..., :k].contiguous(), **cut, state=state, dfinal_state=dfinal)
+        for n, v in g.items():
+            if n in ("du", "ddelta", "dB", "dC", "dz"):
+                assert not v[..., k:].any(), n
+                v = v[..., :k]
+            assert torch.equal(v, h[n]), (n, k)
+    w, b = base.Draw(22)(40, 4), base.Draw(23)(40)
+    st = base.Draw(24)(1, 40, 3, dtype=dtype)
+    for k in (1, 7, 32, 33, L // 2 + 3, L - 1):
+        lens = torch.tensor([k], dtype=torch.int32, device="cuda")
+        far, fdy = base.poison(s["u"], lens), base.poison(dy, lens)
+        near, ndy = s["u"][..., :k].contiguous(), dy[..., :k].contiguous()
+        ends = torch.empty_like(st), torch.empty_like(st)
+        y = swd.short_conv(far, w, b, state=st, final_state=ends[0], lengths=lens)
+        assert torch.equal(y[..., :k], swd.short_conv(near, w, b, state=st, final_state=ends[1]))
+        assert not y[..., k:].any() and torch.equal(*ends)
+        g = swd.short_conv_backward(fdy, far, w, b, state=st, dfinal_state=st, lengths=lens)
+        h = swd.short_conv_backward(ndy, near, w, b, state=st, dfinal_state=st)
+        assert not g[0][..., k:].any() and torch.equal(g[0][..., :k], h[0]) and torch.equal(g[3], h[3])
+        for i in (1, 2):  # sums of at most L terms, each below 2^5, in another order
+            assert float((g[i] - h[i]).abs().max()) <= L * 2.0 ** -23 * 8
