@@ -415,7 +415,11 @@ int spconv_packed_copy_array(const spconv_packed *p, int which, void *dst, int64
  *  - Activations (x, u, delta, z, B, C and their gradients) are of one type,
  *    spconv_dtype; weights (w, bias, A, D, delta_bias), their gradients and
  *    the scan's states are float32.  All arithmetic, sums and states are in
- *    float32; an output is rounded once, when it is stored.
+ *    float32 (spconv_adapter_add says where its factors are cut); an output is
+ *    rounded once, when it is stored.
+ *  - A step size of the scan, or its product with u, that is not finite leaves
+ *    its channel's outputs and states from that position on infinite or NaN;
+ *    which of the two is not specified.
  *  - Input activations are N x C x L with the positions contiguous and any
  *    batch and channel stride (in elements); outputs are contiguous.  A
  *    pointer is aligned to its element type; 16-byte aligned rows run faster.
@@ -551,6 +555,16 @@ int spconv_scan_step(const spconv_scan_args *args, void *stream);
  * and a request with any other index gets out = y.  y holds the shared
  * projection of x (for pruned weights: what spconv_forward wrote).  Adapters
  * of a lower rank than R are padded with zeros.
+ *
+ * With P = 1 everything is float32.  With P > 1 the products go through matrix
+ * instructions, whose running sums are float32 but not rounded to nearest:
+ *  - 16-bit a, x and b are whole in them.  v = a x, a float32 sum, goes into the
+ *    second product with all of its 24 bits for bfloat16, with 22 at least for
+ *    half precision.
+ *  - Of float32 a, x, b and v they take two parts of 11 bits, 22 of 24 bits at
+ *    least, and leave out the product of two second parts: 2^-21 of a term at most.
+ * Sums that are not finite are formed again from whole factors, in float32: what
+ * an infinity or NaN reaches takes up to eight times as long.
  */
 typedef struct spconv_adapter_args {
     int32_t N, P, C, M, R, adapters; /* P positions; R = 1..64                           */

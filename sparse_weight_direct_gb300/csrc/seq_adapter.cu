@@ -133,7 +133,7 @@ struct PromptTile {
     static constexpr int kVec = 16 / sizeof(T);
     // pitches in elements: the eight rows of a matrix read start in different
     // banks; 32-bit fragments take rows 4 (a) and 8 (x) banks apart
-    static constexpr int kXPitch = kWide ? kPos + 8 : kPos + 8;
+    static constexpr int kXPitch = kPos + 8;
     static constexpr int kAPitch = kWide ? kChan + 4 : kChan + 8;
     static constexpr int kXBytes = kChan * kXPitch * (int)sizeof(T);
     static constexpr int kStage = kXBytes + RP * kAPitch * (int)sizeof(T);

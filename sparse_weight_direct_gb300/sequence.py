@@ -14,6 +14,9 @@ default: the current torch stream), and a wrong argument raises SpconvError
 before any work is enqueued.  Like every torch operation, a call on another
 stream waits for nothing: its inputs have to be ready there, and whoever reads
 its outputs elsewhere waits for that stream.
+
+No call records anything for autograd: an input that requires a gradient gives
+an output that does not.  A training step calls the *_backward functions.
 """
 from __future__ import annotations
 
@@ -375,7 +378,11 @@ def adapter_add(y, x, a, b, index, *, scale=None, out=None, stream=None):
     is no adapter (-1).  x: (N, C, P) or, for single tokens, (N, C); y: the
     projection's output, (N, M, P) or (N, M); a: (adapters, R, C) and b:
     (adapters, M, R) of x's type, R = 1..64; index: (N,) int32; scale:
-    (adapters,) float32, 1 if None.  out may be y itself.  Returns out."""
+    (adapters,) float32, 1 if None.  out may be y itself.  Returns out.
+
+    Sums are float32.  Prompts (P > 1) use matrix instructions: float32 factors
+    are good to 2^-21 of each product there, 16-bit ones are whole
+    (include/spconv.h)."""
     if stream is not None:
         return _elsewhere(adapter_add, stream, (y, x, a, b, index), dict(scale=scale, out=out))
     single = getattr(x, "ndim", 0) == 2
