@@ -632,8 +632,9 @@ constexpr int kTokenThreads = 256, kTokenWarps = kTokenThreads / 32;
 // of b, 16 bytes each (with a lane per row a read takes 16 bytes of 32 lines).
 // What does not depend on v -- the first rows of b, of y -- is read before it.
 // What counts is how many reads are under way: 48 tokens, 4096 x 4096, rank 16,
-// bf16 take 6.0 us (two blocks per SM 9.2); 128 of rank 64 take 38 (three
-// blocks 49; four rows of a at a time in three blocks 43).
+// bf16 take 6.0 us (two blocks per SM 9.2); 128 of rank 64 take 31 where they
+// share 16 adapters, 44 with one each (three blocks took 1.29 times as long, with
+// four rows of a at a time 1.13 times).
 template <typename T>
 __global__ void __launch_bounds__(kTokenThreads, 4) token_kernel(const AdapterParams p) {
     __shared__ float part[kMaxR];

@@ -83,7 +83,8 @@ static __device__ __forceinline__ void load_behind(float *s, const T *row, int t
 // instructions are as near a bound as its bytes: a thread per run spent two
 // thirds of them on its place and its weights (82 us on 8 x 4096 x 2048 in
 // bf16), one loop for every case many on the cases (65 us).  So whole, aligned
-// runs of full sequences have a loop of their own (55 us, six blocks per SM).
+// runs of full sequences have a loop of their own (55 us, six blocks per SM, for
+// which 16-bit types with 4 taps spill 40 to 52 bytes).
 template <typename T, int K, bool SILU>
 static __device__ __forceinline__ void conv_whole_runs(const ConvParams &p, const float (&w)[K],
                                                        float b, int c, int t0) {
@@ -317,7 +318,9 @@ static __device__ __forceinline__ void back_whole_runs(const ConvParams &p, cons
 // forms too: K-1 in kVec twice is cheaper than an exchange), writes dx and
 // adds to its sums for dw and db.  The sums are joined in a fixed order.
 // Bound by its instructions: 4 x 2048 x 2048 in bf16 take 28 us, 38 without the
-// loop of its own for whole runs (60 instructions an element).
+// loop of its own for whole runs (60 instructions an element).  That loop is taken
+// where a thread keeps its run from one sequence to the next, so not at every
+// length: 2 x 2048 x 4096, the same bytes, take 40 us.
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads) conv_backward_kernel(const ConvParams p) {
     const int c = blockIdx.x / p.splits, split = blockIdx.x - c * p.splits;

@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(256) join_chunks_kernel(const ScanParams p, in
 // under way: a thread takes one request after the other for its channel, with
 // the next one's states and inputs being read, and its row of A once.  128 x
 // 4096 x 16 in bf16: one request per thread 28 us, two blocks per SM 24, three
-// (B and C kept as words) 18, four spill and take 20.
+// (B and C kept as words) 18, four spill and take 20.  In f32 three spill too (56
+// bytes of stack): 26 us.  32 states and more leave one block: 64 in bf16 72 us.
 template <typename T, int SPT, int LPC>
 __global__ void __launch_bounds__(256, SPT <= 8 ? 3 : 1) scan_step_kernel(const ScanParams p) {
     const int64_t c64 = (int64_t)blockIdx.x * (256 / LPC) + threadIdx.x / LPC;
@@ -608,7 +609,9 @@ int by_lanes(int S, F f) {
 // one takes 0.62 of what it takes among four, two 0.73 (measured: 4096
 // channels x 2048 positions of 2, 3 and 4 sequences take 166, 185 and 205 us).
 // One sequence of those: 4 chunks (512 blocks, one wave) take 93 us, 5 (640) took
-// 131; two sequences whole take 166, in 3 chunks each they took 222.
+// 131; two sequences whole take 166, in 3 chunks each they took 222.  All of it was
+// measured on 16 states in bf16; above 16 states two blocks fit an SM, and a wave
+// counted here runs as two.
 void plan_chunks(ScanParams &p) {
     p.blocks_per_group = (p.per_group + 31) / 32;
     const int64_t blocks = (int64_t)p.groups * p.blocks_per_group * p.N;
