@@ -232,11 +232,13 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const NormParams p) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) s = fmaf(b[k][j], b[k][j], s);
         } else {
+            LongSum all;
             for (int c = c0; c < p.C; c += step) {
                 block(b[0], c);
 #pragma unroll
-                for (int j = 0; j < V; ++j) s = fmaf(b[0][j], b[0][j], s);
+                for (int j = 0; j < V; ++j) all.add(b[0][j], b[0][j]);
             }
+            s = all.value();
         }
         q = rsqrtf(fmaf(total(s, 0), p.inv_C, p.eps));
     }
@@ -257,13 +259,15 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const NormParams p) {
             for (int j = 0; j < V; ++j) s = fmaf(b[k][j], b[k][j], s);
         }
     } else {
+        LongSum all;
         for (int c = c0; c < p.C; c += step) {
             read(kX, x[0], c);
             block(b[0], c);
             sum_up(b[0], x[0], c);
 #pragma unroll
-            for (int j = 0; j < V; ++j) s = fmaf(b[0][j], b[0][j], s);
+            for (int j = 0; j < V; ++j) all.add(b[0][j], b[0][j]);
         }
+        s = all.value();
     }
     if (!p.pre) return;
     const float t = rsqrtf(fmaf(total(s, 1), p.inv_C, p.eps));
@@ -315,26 +319,26 @@ __global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(const NormParam
     };
     float q = 1.f;
     if (p.post) {
-        float s = 0.f;
+        LongSum s;
         for (int c = warp; c < p.C; c += kNormWarps) {
             const float b = block(c);
-            s = fmaf(b, b, s);
+            s.add(b, b);
         }
-        q = rsqrtf(fmaf(total(s), p.inv_C, p.eps));
+        q = rsqrtf(fmaf(total(s.value()), p.inv_C, p.eps));
     }
     const auto sum_of = [&](int c) {
         const float w = p.in[kY] ? (p.post ? p.post[c] : 1.f) * (p.scale ? p.scale[c] : 1.f) : 0.f;
         return in ? fmaf(w, block(c) * q, read(kX, c)) : 0.f;
     };
     const int64_t to = (int64_t)n * p.C * p.L + t;
-    float s = 0.f;
+    LongSum s;
     for (int c = warp; c < p.C; c += kNormWarps) {
         const float v = sum_of(c);
-        s = fmaf(v, v, s);
+        s.add(v, v);
         if (p.sum && t < p.L) static_cast<T *>(p.sum)[to + (int64_t)c * p.L] = from_f32<T>(v);
     }
     if (!p.pre) return;
-    const float f = rsqrtf(fmaf(total(s), p.inv_C, p.eps));
+    const float f = rsqrtf(fmaf(total(s.value()), p.inv_C, p.eps));
     for (int c = warp; c < p.C; c += kNormWarps) {
         const float v = sum_of(c);
         if (t < p.L) static_cast<T *>(p.out)[to + (int64_t)c * p.L] = from_f32<T>(in ? p.pre[c] * (v * f) : 0.f);

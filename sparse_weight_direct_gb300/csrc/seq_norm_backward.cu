@@ -242,11 +242,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const 
         const auto weight = [&](int c) {
             return p.in[kY] ? (p.post ? p.post[c] : 1.f) * (p.scale ? p.scale[c] : 1.f) : 0.f;
         };
-        const auto total = [&](float2 s) {
-            all[0][warp][lane] = s.x;
-            all[1][warp][lane] = s.y;
+        const auto total = [&](const LongSum &x, const LongSum &y) {
+            all[0][warp][lane] = x.value();
+            all[1][warp][lane] = y.value();
             __syncthreads();
-            s = {0.f, 0.f};
+            float2 s{0.f, 0.f};
             for (int w = 0; w < kNormWarps; ++w) {
                 s.x += all[0][w][lane];
                 s.y += all[1][w][lane];
@@ -256,23 +256,23 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const 
         };
         float q = 1.f, f = 0.f, back = 0.f, back_b = 0.f;
         if (p.post) {
-            float2 s{0.f, 0.f};
+            LongSum s, none;
             for (int c = warp; c < p.C; c += kNormWarps) {
                 const float b = block(c);
-                s.x = fmaf(b, b, s.x);
+                s.add(b, b);
             }
-            s = total(s);
-            q = in ? rsqrtf(fmaf(s.x, p.inv_C, p.eps)) : 0.f;
+            q = total(s, none).x;
+            q = in ? rsqrtf(fmaf(q, p.inv_C, p.eps)) : 0.f;
         }
         const auto sum_of = [&](int c) { return fmaf(weight(c), block(c) * q, read(kX, c)); };
         if (p.pre) {
-            float2 s{0.f, 0.f};
+            LongSum squares, slopes;
             for (int c = warp; c < p.C; c += kNormWarps) {
                 const float v = sum_of(c);
-                s.x = fmaf(v, v, s.x);
-                s.y = fmaf(read(kDout, c) * p.pre[c], v, s.y);
+                squares.add(v, v);
+                slopes.add(read(kDout, c) * p.pre[c], v);
             }
-            s = total(s);
+            const float2 s = total(squares, slopes);
             f = in ? rsqrtf(fmaf(s.x, p.inv_C, p.eps)) : 0.f;
             back = f * f * f * (s.y * p.inv_C);
         }
@@ -280,10 +280,10 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const 
             return fmaf(-sum, back, fmaf(f * (p.pre ? p.pre[c] : 0.f), read(kDout, c), read(kDsum, c)));
         };
         const int64_t to = (int64_t)n * p.C * p.L + t;
-        float2 s{0.f, 0.f};
+        LongSum s;
         for (int c = warp; c < p.C; c += kNormWarps) {
             const float sum = sum_of(c), b = block(c), g = grad_of(c, sum);
-            s.x = fmaf(g * weight(c), b, s.x);
+            s.add(g * weight(c), b);
             float a0 = read(kDout, c) * (sum * f), a1 = g * (b * q);
             for (int d = 16; d; d >>= 1) {
                 a0 += __shfl_xor_sync(~0u, a0, d);
@@ -298,8 +298,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const 
         }
         if (!p.in[kY]) continue;
         if (p.post) {
-            s = total(s);
-            back_b = q * q * q * (s.x * p.inv_C);
+            back_b = q * q * q * (total(s, LongSum{}).x * p.inv_C);
         }
         for (int c = warp; c < p.C; c += kNormWarps) {
             const float sum = sum_of(c), b = block(c);
