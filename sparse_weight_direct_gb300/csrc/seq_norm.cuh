@@ -384,21 +384,26 @@ inline int norm_plan(NormParams &p, int dtype, int extra, bool vec) {
             const int rows = kNormThreads / W, run = p.inputs * (vec ? kNormRow : kNormRow + rows * 16);
             const int R = most / (run + extra * kNormThreads);
             if (R < 1) continue;
+            // the smallest cluster whose blocks hold their channels beside the sums and weights
+            const int tile = W * V;
             int ranks = 1;
-            while (ranks < kNormRanks && (int64_t)ranks * rows * R < p.C) ranks *= 2;
-            if ((int64_t)ranks * rows * R < p.C || (W == 8 && ranks > 1)) continue;
+            for (; ranks <= (W == 8 ? 1 : kNormRanks); ranks *= 2) {
+                p.per = (p.C + ranks - 1) / ranks;
+                p.R = (p.per + rows - 1) / rows;
+                if (p.R > R) continue;
+                const int stage = p.R * run;
+                const int rest = (kNormWarps + 2 * (W == 8 ? 1 : kNormRanks)) * sums * tile * 4 + 24 * tile +
+                                 extra * p.R * kNormThreads + rows * p.R * 8;
+                p.stages = 2 * stage + rest <= kNormShared / 2 || stage + rest > kNormShared / 2 ? 2 : 1;
+                if (p.stages * stage + rest > kNormShared) p.stages = 1;
+                p.shared = p.stages * stage + rest;
+                if (p.shared <= kNormShared) break;
+            }
+            if (ranks > (W == 8 ? 1 : kNormRanks)) continue;
             p.ranks = ranks;
-            p.per = (p.C + ranks - 1) / ranks;
-            p.R = (p.per + rows - 1) / rows;
-            p.tiles = (p.L - 1) / (W * V) + 1;
+            p.tiles = (p.L - 1) / tile + 1;
             p.jobs = (int64_t)p.N * p.tiles;
             if (p.jobs > 0x7fff0000) continue;  // (a tile's number and a cluster's step stay within 32 bits)
-            const int tile = W * V, stage = p.R * run;
-            const int rest = (kNormWarps + 2 * (W == 8 ? 1 : kNormRanks)) * sums * tile * 4 + 24 * tile +
-                             extra * p.R * kNormThreads + rows * p.R * 8;
-            p.stages = 2 * stage + rest <= kNormShared / 2 || stage + rest > kNormShared / 2 ? 2 : 1;
-            if (p.stages * stage + rest > kNormShared) p.stages = 1;
-            p.shared = p.stages * stage + rest;
             // (at most; norm_launch takes as many as run at once)
             const int64_t clusters = (int64_t)kSMs * (kNormShared / p.shared < 4 ? kNormShared / p.shared : 4) / ranks;
             p.clusters = (int)(p.jobs < clusters ? p.jobs : clusters);
