@@ -235,8 +235,10 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const NormParams p) {
             LongSum all;
             for (int c = c0; c < p.C; c += step) {
                 block(b[0], c);
+                float part = 0.f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) all.add(b[0][j], b[0][j]);
+                for (int j = 0; j < V; ++j) part = fmaf(b[0][j], b[0][j], part);
+                all.add(part);
             }
             s = all.value();
         }
@@ -264,8 +266,10 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const NormParams p) {
             read(kX, x[0], c);
             block(b[0], c);
             sum_up(b[0], x[0], c);
+            float part = 0.f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) all.add(b[0][j], b[0][j]);
+            for (int j = 0; j < V; ++j) part = fmaf(b[0][j], b[0][j], part);
+            all.add(part);
         }
         s = all.value();
     }
@@ -322,7 +326,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(const NormParam
         LongSum s;
         for (int c = warp; c < p.C; c += kNormWarps) {
             const float b = block(c);
-            s.add(b, b);
+            s.add(b * b);
         }
         q = rsqrtf(fmaf(total(s.value()), p.inv_C, p.eps));
     }
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(const NormParam
     LongSum s;
     for (int c = warp; c < p.C; c += kNormWarps) {
         const float v = sum_of(c);
-        s.add(v, v);
+        s.add(v * v);
         if (p.sum && t < p.L) static_cast<T *>(p.sum)[to + (int64_t)c * p.L] = from_f32<T>(v);
     }
     if (!p.pre) return;

@@ -61,18 +61,6 @@ static __device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
     return pack2(rcp(e.x), rcp(e.y));
 }
 
-// A thread's sum of many products, with what its additions lost: 131,072 squares of
-// 1.1 added to one float are 3e-3 off.
-struct LongSum {
-    float s = 0.f, lost = 0.f;
-    __device__ __forceinline__ void add(float a, float b) {
-        const float v = __fmul_rn(a, b), t = __fadd_rn(s, v), part = __fsub_rn(t, s);
-        lost += __fadd_rn(__fsub_rn(s, __fsub_rn(t, part)), __fsub_rn(v, part));
-        s = t;
-    }
-    __device__ __forceinline__ float value() const { return lost == lost ? s + lost : s; }  // (infinity stays)
-};
-
 // ---------------------------------------------------------------- a tile's sums
 
 // Shared memory behind the stages.

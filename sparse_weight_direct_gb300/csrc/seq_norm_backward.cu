@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const 
             LongSum s, none;
             for (int c = warp; c < p.C; c += kNormWarps) {
                 const float b = block(c);
-                s.add(b, b);
+                s.add(b * b);
             }
             q = total(s, none).x;
             q = in ? rsqrtf(fmaf(q, p.inv_C, p.eps)) : 0.f;
@@ -269,8 +269,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const 
             LongSum squares, slopes;
             for (int c = warp; c < p.C; c += kNormWarps) {
                 const float v = sum_of(c);
-                squares.add(v, v);
-                slopes.add(read(kDout, c) * p.pre[c], v);
+                squares.add(v * v);
+                slopes.add(read(kDout, c) * p.pre[c] * v);
             }
             const float2 s = total(squares, slopes);
             f = in ? rsqrtf(fmaf(s.x, p.inv_C, p.eps)) : 0.f;
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_wide_kernel(const 
         LongSum s;
         for (int c = warp; c < p.C; c += kNormWarps) {
             const float sum = sum_of(c), b = block(c), g = grad_of(c, sum);
-            s.add(g * weight(c), b);
+            s.add(g * weight(c) * b);
             float a0 = read(kDout, c) * (sum * f), a1 = g * (b * q);
             for (int d = 16; d; d >>= 1) {
                 a0 += __shfl_xor_sync(~0u, a0, d);
