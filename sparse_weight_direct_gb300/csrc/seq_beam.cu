@@ -280,12 +280,16 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamParams p)
     for (int b = warp; b < p.B; b += kWarps) {
         const float2 *sums = p.sums + (rows + b) * p.parts;
         float2 s = lane < p.parts ? sums[lane] : make_float2(-kLargest, 0.f);
+        LongSum sum_of{s.y};  // (thousands of parts alike would all be rounded to the same side)
         for (int o = lane + 32; o < p.parts; o += 32) {
             const float2 u = sums[o];
-            const float top = fmaxf(s.x, u.x);
-            s.y = s.y * ex2((s.x - top) * kLog2e) + u.y * ex2((u.x - top) * kLog2e);
+            const float top = fmaxf(s.x, u.x), fall = ex2((s.x - top) * kLog2e);
+            sum_of.s *= fall;
+            sum_of.lost *= fall;
+            sum_of.add(u.y * ex2((u.x - top) * kLog2e));
             s.x = top;
         }
+        s.y = sum_of.value();
         float most = s.x;
         for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
         float sum = s.y * ex2((s.x - most) * kLog2e);
