@@ -23,6 +23,7 @@ an output that does not.  A training step calls the *_backward functions.
 from __future__ import annotations
 
 import ctypes
+import operator
 import struct
 from array import array
 
@@ -629,23 +630,26 @@ def beam_select(logits, scores, *, beams=None, eos=None, ended=None, stream=None
         return _elsewhere(beam_select, stream, (logits, scores), dict(beams=beams, eos=eos, ended=ended))
     dt, code, dev = _begin(logits, "logits", 3)
     N, B, V = logits.shape
-    K = B if beams is None else beams
+    try:
+        K = B if beams is None else operator.index(beams)
+        token = -1 if eos is None else operator.index(eos)
+    except (TypeError, ValueError) as error:
+        _fail(f"beams and eos must be whole numbers ({error})")
     if eos is None:
-        eos = -1
         if ended is not None:
             _fail("ended beams need eos")
-    elif not 0 <= eos < V:
+    elif not 0 <= token < V:
         _fail("eos must be one of the vocabulary's tokens")
-    if not isinstance(K, int) or not 1 <= K <= 32:
+    if not 1 <= K <= 32:
         _fail("1 to 32 beams can be selected")
     if scores is None:
         _fail("scores must be given")
     at, strides = _rows(logits, "logits", dt, dev, logits.shape)
     chosen = (N, K)
     new_scores, tokens, parents = _new(chosen, _f32, dev), _new(chosen, _i32, dev), _new(chosen, _i32, dev)
-    new_ended = _new(chosen, _bool, dev) if eos >= 0 else None
+    new_ended = _new(chosen, _bool, dev) if eos is not None else None
     try:
-        args = _pack_beam(N, B, V, K, code, eos, strides[0], strides[1], at, _whole(scores, "scores", _f32, dev, (N, B)),
+        args = _pack_beam(N, B, V, K, code, token, strides[0], strides[1], at, _whole(scores, "scores", _f32, dev, (N, B)),
                           _whole(ended, "ended", _bool, dev, (N, B)), new_scores.data_ptr(), tokens.data_ptr(),
                           parents.data_ptr(), 0 if new_ended is None else new_ended.data_ptr())
     except struct.error as error:

@@ -1,12 +1,13 @@
 """Beam search's selection at sizes and arguments beyond those of test_beams.py."""
 import math
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import sparse_weight_direct_gb300 as swd  # noqa: E402
-from test_sequence import F16  # noqa: E402
+from test_sequence import F16, Draw  # noqa: E402
 
 
 @pytest.mark.gpu
@@ -29,3 +30,17 @@ def test_sums_of_parts_that_round_alike():
         score, token, _, _ = swd.beam_select(logits, start)
         assert int(token) == 0
         assert abs(float(score) - (float(start) - exact)) <= 47 * 2.0 ** -24, low
+
+
+@pytest.mark.gpu
+def test_beams_and_eos_of_any_kind_of_whole_number():
+    d = Draw(23)
+    logits, scores = d(2, 3, 40), d(2, 3)
+    want = swd.beam_select(logits, scores, beams=4, eos=7)
+    for beams, eos in ((np.int64(4), np.int32(7)), (torch.tensor(4), torch.tensor(7))):
+        assert all(torch.equal(a, b) for a, b in zip(swd.beam_select(logits, scores, beams=beams, eos=eos), want))
+    for bad in ("2", 2.0, [2], None.__class__, torch.tensor([1, 2])):
+        with pytest.raises(swd.SpconvError):
+            swd.beam_select(logits, scores, eos=bad)
+        with pytest.raises(swd.SpconvError):
+            swd.beam_select(logits, scores, beams=bad)
