@@ -595,7 +595,8 @@ int spconv_adapter_add(const spconv_adapter_args *args, void *stream);
  * h starts from state (zeros without one); final_state is h behind the
  * sequence's last position.  1 - a^2 keeps its digits where a is next to one.
  * Where a is one (A * rho is zero), the root's slope is taken as zero.  A
- * positive A gives NaN, and so does an A of minus infinity where rho is zero.  An
+ * positive A gives NaN, and so does an A of minus infinity where rho is zero (and in
+ * dr and dr_bias, whose formula has zero times infinity there).  An
  * x, r or i that is not finite leaves its channel's outputs and states from that
  * position on infinite or NaN, but for infinite r and i, whose gates are 0 or 1.
  */
@@ -647,8 +648,11 @@ int spconv_gated_scan_step(const spconv_gated_scan_args *args, void *stream);
  *
  * x or y is given, or both; z, post and scale belong to y, and `sum` is written
  * if and only if y is given.  out comes from the sum as it is before its
- * rounding.  Squares and their sums are float32: a position whose values are
- * beyond 2^63 gives zeros or NaN.  One position of each of N requests is L = 1
+ * rounding.  Squares and their sums over the channels are float32: where the sum
+ * of x^2, of b^2 or of (scale post b)^2 at a position is beyond 2^128 (values alike
+ * from 2^64 / sqrt(C) on), its outputs and gradients are zeros, infinite or NaN, the
+ * sum's norm also where only one of its terms is that large.  With eps = 0 that holds
+ * for sums of squares below 2^-126 too.  One position of each of N requests is L = 1
  * with the channels' stride 1.  x and y may be the same tensor.  Which inputs are
  * NULL has to be the same for the workspace's size as for the call.
  */
@@ -694,7 +698,7 @@ int spconv_residual_norm_backward(const spconv_residual_norm_args *args, void *s
  * token is eos.  NaN counts as minus infinity and infinity as the largest
  * float32, in logits and scores.
  * Totals are formed and compared in 64 bits, from float32 exponentials whose
- * sum is good to about 2^-22 relative; new_scores are rounded once.
+ * sum is good to about 2^-21 relative for any V; new_scores are rounded once.
  */
 typedef struct spconv_beam_select_args {
     int32_t N, B, V, K, dtype;     /* 1 <= B, K <= 32, V >= 1, B * V < 2^31             */

@@ -118,7 +118,9 @@ __global__ void __launch_bounds__(kGatedThreads, sizeof(T) == 4 ? 2 : 3) gated_k
             mine.w = unpack2(w_sum).x + unpack2(w_sum).y;
             done = w_min > Decay::kNear;
         }
-        if (!done) {  // the ends of a sequence, decays far from one
+        // the ends of a sequence, decays far from one (formed again, one by one: with A
+        // from -8 on instead of -0.1 8 x 4096 x 2048 in bf16 take 193 us instead of 133)
+        if (!done) {
             mine.w = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {

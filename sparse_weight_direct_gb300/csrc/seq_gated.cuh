@@ -158,7 +158,8 @@ static __device__ __forceinline__ f32x2 sigmoid2(f32x2 v, f32x2 unit, f32x2 bias
     const float2 e = unpack2(add2(ex2_2(fma2(v, unit, bias)), pack2(1.f, 1.f)));
     return pack2(rcp(e.x), rcp(e.y));
 }
-// a = 2^w for w in [-0.75, 0], 1 - a^2 and the inverse of its root (0 for 0).
+// a = 2^w for w in [-0.75, 0], 1 - a^2 and the inverse of its root (for 0 some finite
+// number: of no consequence times the square, to be replaced where it stands alone).
 // 1 - a comes from Decay's polynomial, so that 1 - a^2 keeps its digits next to a
 // decay of one; a itself is rounded once.
 struct Decay2 {
@@ -186,7 +187,7 @@ struct Decay2 {
 // block, and few rows clusters as far as they take a row in one round, since with
 // more rounds a third of what it reads is read again.  (160 rows of 8192 in bf16: 17 us in
 // clusters, 20 in rounds; 249 of 17,042 in float32, two rounds of a cluster: 138 and 70 us;
-// 504 of 27,506 in f16: 179 and 90 us.)
+// 504 of 27,506 in f16 without gates: 179 and 91 us, with both 132 in rounds.)
 inline void gated_plan(GatedParams &p, int V, bool aligned, bool whole) {
     const int64_t runs = ((int64_t)p.L + (aligned ? 0 : V - 1) + V - 1) / V;
     p.log_tx = 2;

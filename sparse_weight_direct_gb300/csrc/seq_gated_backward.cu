@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_backward_kernel(const 
             }
             const float h_round = rounds > 1 ? p.carry[g.row * rounds + k] : start;
 
-            // each position's gates, decay, sqrt(1 - a^2) and its inverse (0 for 0), and
-            // the gradient that its own output gives its state
+            // each position's gates, decay, sqrt(1 - a^2) and its inverse (for 0 replaced
+            // below), and the gradient that its own output gives its state
             float rho[V], iota[V], zeta[V], a[V], m[V], inverse[V], dh[V];
             Both mine{0.f, 0.f, 0.f};
             bool done = false;
@@ -249,7 +249,9 @@ __global__ void __launch_bounds__(kGatedThreads, 2) gated_backward_kernel(const 
                 mine.w = unpack2(w_sum).x + unpack2(w_sum).y;
                 done = w_min > Decay::kNear;
             }
-            if (!done) {  // the ends of a sequence, decays far from one
+            // the ends of a sequence, decays far from one (formed again, one by one: with
+            // A from -8 on instead of -0.1 4 x 2048 x 2048 in bf16 take 102 us instead of 92)
+            if (!done) {
                 mine.w = 0.f;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {

@@ -297,7 +297,9 @@ __global__ void __launch_bounds__(1024) norm_token_kernel(const NormParams p) {
 }
 
 // More channels than a cluster holds: a block for 32 positions, whose rows are
-// read again (from the cache where they fit) for each sum.
+// read again (from the cache where they fit) for each sum.  Few blocks, each with one
+// load of 64 or 128 bytes a warp on its way: 4 x 15,400 x 512 in bf16 take 3.2 ms (15,360
+// channels, in clusters, 0.146).
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_wide_kernel(const NormParams p) {
     __shared__ float sums[kNormWarps][33];
